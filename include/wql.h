@@ -279,6 +279,136 @@ wql_status wql_topk_rescore(const void* x, int32_t x_dtype, int64_t m,
 wql_status wql_embed_gather(const int32_t* ids, int64_t t, const wql_weight* w,
                             int32_t out_dtype, void* out, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the head: the norm before it, a head in microscaled codes, and the
+ * draw of the next token after it.  (No counterpart on the pages.)
+ * ------------------------------------------------------------------------- */
+
+/* Microscaled codes (OCP Microscaling Formats): blocks of 32 consecutive
+ * columns of a row share one power-of-two scale. */
+typedef enum wql_mx_format {
+  WQL_MX_FP4 = 0,  /* e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+  WQL_MX_FP8 = 1   /* e4m3 ("fn": no infinities, largest finite 448) */
+} wql_mx_format;
+
+/* A matrix in microscaled codes: value = code value * 2^(scale byte - 127).
+ *   codes   FP4: uint8 [rows, k/2], element 2i of a row in the low nibble of
+ *           byte i, element 2i + 1 in the high one; FP8: uint8 [rows, k].
+ *   scales  uint8 (e8m0: 2^(byte - 127), 255 = NaN) in tiles of 128 rows x 4
+ *           blocks (128 columns), tiles row-major over [ceil(rows/128),
+ *           ceil(k/128)], 512 bytes each: row r, block b of a tile at byte
+ *           16 * (r % 32) + 4 * (r / 32) + b.  This is the order in which the
+ *           tensor cores take them.  Bytes past the last row or block are 0.
+ * Requirements: k % 32 == 0; codes and scales 16-byte aligned; rows < 2^31. */
+typedef struct wql_mx {
+  int32_t format;      /* wql_mx_format */
+  int32_t reserved;    /* 0 */
+  int64_t rows;
+  int64_t k;
+  const void* codes;   /* device */
+  const void* scales;  /* device, wql_mx_scale_bytes(rows, k) bytes */
+} wql_mx;
+
+/* Bytes of the scale tiles of a [rows, k] matrix (0 for bad sizes).  Host
+ * arithmetic. */
+size_t wql_mx_scale_bytes(int64_t rows, int64_t k);
+
+/* Quantise [rows, k] to microscaled codes.  Per block of 32 columns:
+ *   e    = floor(log2(max |x|)) - 2 (FP4) or - 8 (FP8), at least -127
+ *          (a block of zeros: -127),
+ *   code = x / 2^e rounded to nearest, ties to even, saturated at 6 or 448.
+ * A block with a NaN or an infinity gets the scale NaN (byte 255); its codes
+ * are 0 (FP4) or NaN (FP8).
+ *   x           device [rows, k] of x_dtype (F32, F16 or BF16), 16-byte aligned
+ *   codes_out   device, layout of wql_mx
+ *   scales_out  device, wql_mx_scale_bytes(rows, k) bytes, all of them written
+ * Bit-exact with the definition. */
+wql_status wql_mx_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t k,
+                           int32_t format, void* codes_out, void* scales_out,
+                           cudaStream_t stream);
+
+/* The values of a microscaled matrix: out device [rows, k] of out_dtype (F32,
+ * F16 or BF16), 16-byte aligned; the product of code and scale, exact in fp32,
+ * rounded once to nearest-even. */
+wql_status wql_mx_dequantize(const wql_mx* a, int32_t out_dtype, void* out,
+                             cudaStream_t stream);
+
+/* Logits of a microscaled head: logits[m, n] = sum_k x[m, k] * w[n, k]
+ * (+ bias[n]), the products of the codes' values exact, the sums in fp32.
+ *   x          FP4 or FP8, [m, k] (rows = m)
+ *   w          FP4, [n, k] (rows = n), the same k
+ *   bias       device [n] of out_dtype, or NULL
+ *   logits_out device [m, n] of out_dtype (F16 or BF16), rounded to nearest-even
+ *   workspace  device, 256-byte aligned, zero-filled once, ws_bytes >=
+ *              wql_workspace_size(m, n, 0), or NULL.  A bounded wait of the
+ *              kernel that runs out records bit 8 in its error word (bytes
+ *              4..7, sticky); with NULL it is not recorded.
+ * A NaN scale (or an fp8 NaN code) gives NaN logits for its row or column. */
+wql_status wql_mx_logits(const wql_mx* x, const wql_mx* w, const void* bias,
+                         int32_t out_dtype, void* logits_out, void* workspace,
+                         size_t ws_bytes, cudaStream_t stream);
+
+/* What wql_add_rmsnorm writes. */
+typedef enum wql_norm_out {
+  WQL_NORM_SAME = 0,    /* out [m, k] of the input's dtype; scales_out unused */
+  WQL_NORM_E4M3 = 1,    /* out uint8 e4m3 [m, k]; scales_out float [m] */
+  WQL_NORM_MX_FP8 = 2,  /* out, scales_out: the codes and scales of a wql_mx */
+  WQL_NORM_MX_FP4 = 3
+} wql_norm_out;
+
+/* Residual addition and root-mean-square norm, in fp32 up to the outputs:
+ *   h = x + residual (x alone when residual is NULL),
+ *   residual_out = RN(h),
+ *   y = h * rsqrt(mean_k(h^2) + eps) * gamma,
+ * and y is written as out_format says, rounded once:
+ *   E4M3       s = max(max_k |y| *f32 fl32(1/448), 1e-8f),
+ *              code = RN_e4m3(clamp(y /f32 s, -448, 448)); a NaN in a row
+ *              makes its scale NaN
+ *   MX_FP8/4   as wql_mx_quantize
+ *   x, residual   device [m, k] of dtype (F16 or BF16)
+ *   gamma         device [k] of dtype
+ *   residual_out  device [m, k] of dtype, or NULL; may be residual or x
+ *   out           may be x or residual for SAME
+ * k <= 65536; k % 32 == 0 for the MX outputs, any k otherwise.  Pointers are
+ * aligned to their elements (16 bytes for the MX outputs' tensors; 16-byte
+ * aligned tensors with k % 8 == 0 run faster). */
+wql_status wql_add_rmsnorm(const void* x, const void* residual, const void* gamma,
+                           int32_t dtype, int64_t m, int64_t k, float eps,
+                           int32_t out_format, void* out, void* scales_out,
+                           void* residual_out, cudaStream_t stream);
+
+/* Largest vocabulary of wql_sample (its integer sums stay below 2^53). */
+#define WQL_SAMPLE_MAX_N (1 << 22)
+
+/* Draw one token id per row of logits.  Per row, with l the logits (a NaN
+ * counts as -inf), t the temperature and u the given random number:
+ *   t <= 0 or NaN: the lowest index of the largest logit, logp = 0.  Else
+ *   e_i = exp2((l_i - max l) *f32 c) with c = fl32(log2 e) /f32 t,
+ *   W_i = floor(2^31 e_i), an integer, so that every sum of weights below is
+ *         exact and does not depend on the order in which it is taken;
+ *   the tokens are ranked by logit descending, then index ascending;
+ *   top_k  in 1..n-1 keeps the first top_k (anything else keeps all);
+ *   top_p  < 1 keeps those before which the kept weights sum to less than
+ *          top_p * (the sum over all that top_k keeps), and the first;
+ *   min_p  > 0 keeps those with e_i >= min(min_p, 1);
+ *   r = floor(u * sum of the kept W), limited to [0, sum); the id is the
+ *   lowest index at which the running sum over the kept W, by index, exceeds
+ *   r; logp = log(W_id / sum).
+ * A row without a logit above -inf gives id -1 and logp NaN.  (Tokens less
+ * likely than 2^-31 of the likeliest have W = 0 and are never drawn.)
+ *   logits       device [m, n] of dtype (F32, F16 or BF16), 16-byte aligned
+ *   u            device float [m], in [0, 1)
+ *   temperature  device float [m], or NULL: 1
+ *   top_k        device int32 [m], or NULL: off
+ *   top_p, min_p device float [m], or NULL: off
+ *   ids_out      device int32 [m]
+ *   logp_out     device float [m], or NULL
+ * 1 <= n <= WQL_SAMPLE_MAX_N. */
+wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n,
+                      const float* u, const float* temperature, const int32_t* top_k,
+                      const float* top_p, const float* min_p, int32_t* ids_out,
+                      float* logp_out, cudaStream_t stream);
+
 /* Static text for a status code. */
 const char* wql_status_string(wql_status status);
 

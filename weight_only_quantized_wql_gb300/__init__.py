@@ -14,6 +14,12 @@ Functions
              candidates_only=False)             -> (logits, topk_idx, topk_val)
   wql_topk_rescore(x, w_ref, topk_idx, topk_val, logits, bias=None)
   wql_embed_gather(ids, qw, out_dtype=torch.float16, out=None) -> [*ids.shape, k]
+  wql_add_rmsnorm(x, gamma, residual=None, eps=1e-6, fmt=NORM_SAME)
+                                            -> (y, residual_out, scales)
+  wql_mx_quantize(x, fmt) -> MXMatrix;  wql_mx_dequantize(a, out_dtype)
+  wql_mx_logits(x, w, out_dtype, bias=None)         -> logits
+  wql_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None)
+                                            -> (ids, logp)
   wql_status_string, wql_last_error, wql_launch_count
 """
 from __future__ import annotations
@@ -30,16 +36,21 @@ from . import _build
 __all__ = [
     "WQLError", "QuantizedWeight", "Workspace", "load", "wql_quantize", "wql_pack",
     "wql_unpack", "wql_workspace_size", "wql_logits", "wql_logits_noalloc", "wql_topk_rescore",
-    "wql_embed_gather", "wql_debug_set_waits",
+    "wql_embed_gather", "MXMatrix", "wql_mx_scale_bytes", "wql_mx_quantize", "wql_mx_dequantize",
+    "wql_mx_logits", "wql_add_rmsnorm", "wql_sample", "wql_debug_set_waits",
     "wql_status_string", "wql_last_error", "wql_launch_count", "F32", "F16", "BF16",
     "CLIP_RTN", "CLIP_MSE", "MAX_TOPK", "NOALLOC_SCRATCH_BYTES", "FMT_SYM", "FMT_E4M3",
-    "FMT_ASYM",
+    "FMT_ASYM", "MX_FP4", "MX_FP8", "NORM_SAME", "NORM_E4M3", "NORM_MX_FP8", "NORM_MX_FP4",
+    "SAMPLE_MAX_N",
 ]
 
 F32, F16, BF16 = 0, 1, 2
 CLIP_RTN, CLIP_MSE = 0, 1
 FMT_SYM, FMT_E4M3, FMT_ASYM = 0, 1, 2    # wql_format
 WEIGHT_STATIC = 0x100                    # flag ORed into the format field
+MX_FP4, MX_FP8 = 0, 1                    # wql_mx_format
+NORM_SAME, NORM_E4M3, NORM_MX_FP8, NORM_MX_FP4 = 0, 1, 2, 3    # wql_norm_out
+SAMPLE_MAX_N = 1 << 22
 MAX_TOPK = 16
 MAX_CTAS = 1024
 _DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -68,6 +79,12 @@ class _WqlWeight(ctypes.Structure):
                 ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("qweight", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zeros", ctypes.c_void_p)]
+
+
+class _WqlMx(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -109,6 +126,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                          vp]
         lib.wql_embed_gather.restype = i32
         lib.wql_embed_gather.argtypes = [vp, i64, ctypes.POINTER(_WqlWeight), i32, vp, vp]
+        mx = ctypes.POINTER(_WqlMx)
+        lib.wql_mx_scale_bytes.restype = sz
+        lib.wql_mx_scale_bytes.argtypes = [i64, i64]
+        lib.wql_mx_quantize.restype = i32
+        lib.wql_mx_quantize.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+        lib.wql_mx_dequantize.restype = i32
+        lib.wql_mx_dequantize.argtypes = [mx, i32, vp, vp]
+        lib.wql_mx_logits.restype = i32
+        lib.wql_mx_logits.argtypes = [mx, mx, vp, i32, vp, vp, sz, vp]
+        lib.wql_add_rmsnorm.restype = i32
+        lib.wql_add_rmsnorm.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_float, i32, vp, vp,
+                                        vp, vp]
+        lib.wql_sample.restype = i32
+        lib.wql_sample.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.wql_status_string.restype = ctypes.c_char_p
         lib.wql_status_string.argtypes = [i32]
         lib.wql_last_error.restype = ctypes.c_char_p
@@ -405,3 +436,176 @@ def wql_embed_gather(ids: torch.Tensor, qw: QuantizedWeight, out_dtype=torch.flo
     _check("wql_embed_gather", lib.wql_embed_gather(
         _ptr(flat), t, ctypes.byref(st), _DTYPE_CODE[out.dtype], _ptr(out), _stream(ids.device)))
     return out.reshape(*ids.shape, qw.k)
+
+
+@dataclass
+class MXMatrix:
+    """A matrix in microscaled codes, in the layout wql.h documents (wql_mx)."""
+    codes: torch.Tensor        # uint8 [rows, k/2] (MX_FP4) or [rows, k] (MX_FP8)
+    scales: torch.Tensor       # uint8 scale tiles [ceil(rows/128), ceil(k/128), 512]
+    fmt: int                   # MX_FP4 or MX_FP8
+    rows: int
+    k: int
+
+    def _struct(self) -> _WqlMx:
+        return _WqlMx(self.fmt, 0, self.rows, self.k, self.codes.data_ptr(),
+                      self.scales.data_ptr())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def wql_mx_scale_bytes(rows: int, k: int) -> int:
+    return int(load().wql_mx_scale_bytes(rows, k))
+
+
+def _mx_empty(rows: int, k: int, fmt: int, device) -> MXMatrix:
+    if fmt not in (MX_FP4, MX_FP8):
+        raise ValueError("fmt must be MX_FP4 or MX_FP8")
+    codes = torch.empty((rows, k // 2 if fmt == MX_FP4 else k), dtype=torch.uint8, device=device)
+    scales = torch.empty((-(-rows // 128), -(-k // 128), 512), dtype=torch.uint8, device=device)
+    return MXMatrix(codes, scales, fmt, rows, k)
+
+
+def _mx_check(a: MXMatrix, name: str):
+    for t, part in ((a.codes, "codes"), (a.scales, "scales")):
+        _cuda(t, f"{name}.{part}")
+        if t.dtype != torch.uint8:
+            raise ValueError(f"{name}.{part} must be uint8")
+    if a.codes.numel() != a.rows * (a.k // 2 if a.fmt == MX_FP4 else a.k):
+        raise ValueError(f"{name}.codes does not hold {a.rows} x {a.k} codes")
+    if a.scales.numel() != -(-a.rows // 128) * -(-a.k // 128) * 512:
+        raise ValueError(f"{name}.scales does not hold the scale tiles of {a.rows} x {a.k}")
+
+
+def wql_mx_quantize(x: torch.Tensor, fmt: int = MX_FP4) -> MXMatrix:
+    """Microscaled codes of x (fp32/fp16/bf16); leading dimensions are
+    flattened to rows (see wql.h)."""
+    lib = load()
+    x2 = x.reshape(-1, x.shape[-1])
+    _cuda(x2, "x")
+    rows, k = x2.shape
+    a = _mx_empty(rows, k, fmt, x.device)
+    _check("wql_mx_quantize", lib.wql_mx_quantize(
+        x2.data_ptr(), _DTYPE_CODE[x.dtype], rows, k, fmt, a.codes.data_ptr(),
+        a.scales.data_ptr(), _stream(x.device)))
+    return a
+
+
+def wql_mx_dequantize(a: MXMatrix, out_dtype=torch.float32) -> torch.Tensor:
+    """The values [rows, k] that microscaled codes stand for."""
+    lib = load()
+    _mx_check(a, "a")
+    out = torch.empty((a.rows, a.k), dtype=out_dtype, device=a.codes.device)
+    _check("wql_mx_dequantize", lib.wql_mx_dequantize(
+        ctypes.byref(a._struct()), _DTYPE_CODE[out_dtype], out.data_ptr(),
+        _stream(a.codes.device)))
+    return out
+
+
+def wql_mx_logits(x: MXMatrix, w: MXMatrix, out_dtype=torch.bfloat16,
+                  bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: Workspace | None = None) -> torch.Tensor:
+    """logits [x.rows, w.rows] of a microscaled head: x MX_FP8 or MX_FP4, w
+    MX_FP4 (see wql.h).  With a workspace, a wait that runs out is recorded in
+    its error word."""
+    lib = load()
+    _mx_check(x, "x")
+    _mx_check(w, "w")
+    dev = x.codes.device
+    if out is None:
+        out = torch.empty((x.rows, w.rows), dtype=out_dtype, device=dev)
+    else:
+        _cuda(out, "out")
+        if out.dtype != out_dtype or out.numel() != x.rows * w.rows:
+            raise ValueError("out must be [x.rows, w.rows] of out_dtype")
+    if bias is not None:
+        _cuda(bias, "bias")
+        if bias.dtype != out_dtype or bias.numel() != w.rows:
+            raise ValueError("bias must be [w.rows] of out_dtype")
+    ws = workspace.get(wql_workspace_size(x.rows, w.rows, 0)) if workspace is not None else None
+    _check("wql_mx_logits", lib.wql_mx_logits(
+        ctypes.byref(x._struct()), ctypes.byref(w._struct()),
+        bias.data_ptr() if bias is not None else None, _DTYPE_CODE[out_dtype], out.data_ptr(),
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _stream(dev)))
+    return out
+
+
+def wql_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
+                    eps: float = 1e-6, fmt: int = NORM_SAME,
+                    residual_out: torch.Tensor | None = None):
+    """(y, residual_out, scales) of h = x + residual and its RMS norm times
+    gamma (see wql.h).  residual_out is h in x's dtype (None without a
+    residual, unless one is passed; it may be `residual` itself).  y is in x's
+    dtype (NORM_SAME, scales None), float8_e4m3fn with a float32 scale per row
+    (NORM_E4M3), or an MXMatrix (NORM_MX_FP8 / NORM_MX_FP4, scales None)."""
+    lib = load()
+    x2 = x.reshape(-1, x.shape[-1])
+    _cuda(x2, "x")
+    m, k = x2.shape
+    _cuda(gamma, "gamma")
+    if gamma.dtype != x.dtype or gamma.numel() != k:
+        raise ValueError("gamma must be [k] of x's dtype")
+    if residual is not None:
+        _cuda(residual, "residual")
+        if residual.dtype != x.dtype or residual.numel() != m * k:
+            raise ValueError("residual must have x's shape and dtype")
+        if residual_out is None:
+            residual_out = torch.empty_like(x2).view(x.shape)
+    if residual_out is not None:
+        _cuda(residual_out, "residual_out")
+        if residual_out.dtype != x.dtype or residual_out.numel() != m * k:
+            raise ValueError("residual_out must have x's shape and dtype")
+    scales = None
+    if fmt == NORM_SAME:
+        y = codes = torch.empty_like(x2).view(x.shape)
+    elif fmt == NORM_E4M3:
+        y = codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    elif fmt in (NORM_MX_FP8, NORM_MX_FP4):
+        y = _mx_empty(m, k, MX_FP8 if fmt == NORM_MX_FP8 else MX_FP4, x.device)
+        codes = y.codes
+    else:
+        raise ValueError("fmt must be one of NORM_SAME, NORM_E4M3, NORM_MX_FP8, NORM_MX_FP4")
+    sc = y.scales if isinstance(y, MXMatrix) else scales
+    _check("wql_add_rmsnorm", lib.wql_add_rmsnorm(
+        x2.data_ptr(), residual.data_ptr() if residual is not None else None, gamma.data_ptr(),
+        _DTYPE_CODE[x.dtype], m, k, eps, fmt, codes.data_ptr(),
+        sc.data_ptr() if sc is not None else None,
+        residual_out.data_ptr() if residual_out is not None else None, _stream(x.device)))
+    return y, residual_out, scales
+
+
+def _row_param(t, name: str, dtype, m: int, device):
+    if t is None:
+        return None
+    _cuda(t, name)
+    if t.dtype != dtype or t.numel() != m or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of {m} elements on {device}")
+    return t.data_ptr()
+
+
+def wql_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+               top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+               min_p: torch.Tensor | None = None):
+    """(ids int32, logp float32) drawn from each row of logits [*, n] with the
+    random number u in [0, 1) of that row; the filters are tensors with a value
+    per row (see wql.h).  A row without a logit above -inf gives (-1, NaN)."""
+    lib = load()
+    l2 = logits.reshape(-1, logits.shape[-1])
+    _cuda(l2, "logits")
+    m, n = l2.shape
+    dev = logits.device
+    f32 = torch.float32
+    pu = _row_param(u, "u", f32, m, dev)
+    if pu is None:
+        raise ValueError("u must be given")
+    ids = torch.empty(logits.shape[:-1], dtype=torch.int32, device=dev)
+    logp = torch.empty(logits.shape[:-1], dtype=f32, device=dev)
+    _check("wql_sample", lib.wql_sample(
+        l2.data_ptr(), _DTYPE_CODE[logits.dtype], m, n, pu,
+        _row_param(temperature, "temperature", f32, m, dev),
+        _row_param(top_k, "top_k", torch.int32, m, dev), _row_param(top_p, "top_p", f32, m, dev),
+        _row_param(min_p, "min_p", f32, m, dev), ids.data_ptr(), logp.data_ptr(), _stream(dev)))
+    return ids, logp

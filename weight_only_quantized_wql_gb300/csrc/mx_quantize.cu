@@ -1,0 +1,195 @@
+// mx_quantize.cu -- microscaled codes from dense rows, and back.
+//
+// Per block of 32 columns: scale 2^e with e = floor(log2 max|x|) - emax (2 for
+// e2m1, 8 for e4m3), codes x / 2^e rounded to nearest even.  Division by a
+// power of two is exact, so the only rounding is the code's.
+//
+// HBM-bound: quantising reads 2 (4) bytes an element and writes 17/32 (FP4)
+// or 33/32 (FP8).  A thread takes eight columns (one 16-byte load of 16-bit
+// input), four lanes a block, a half warp one scale tile's row (128 columns),
+// so the codes of a half warp are 64 or 128 consecutive bytes and its four
+// scales one word.  Loads of several tiles are in flight per thread before
+// the first is used.
+#include "mx.cuh"
+
+namespace wql {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHalfWarps = kThreads / 16;
+constexpr int kUnroll = 4;
+
+template <typename T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = ldg_stream_u4(p);
+    const T* h = reinterpret_cast<const T*>(&a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(h[i]);
+  }
+}
+
+// A block of threads takes `rows_per_cta` rows (of the rows padded to 128, so
+// that every byte of the scale tiles is written) and all their tile columns.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+    mx_quantize_kernel(const MxQuantizeArgs a, int tile_cols, int padded_rows, int rows_per_cta) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  const int row0 = blockIdx.x * rows_per_cta;
+  const int items = min(rows_per_cta, padded_rows - row0) * tile_cols;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  // every half warp makes the same number of passes (the shuffles need whole warps)
+  for (int i0 = 0; i0 < items; i0 += kUnroll * kHalfWarps) {
+    float v[kUnroll][8];
+    int row[kUnroll], tc[kUnroll];
+    bool in[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int item = i0 + u * kHalfWarps + hw;
+      row[u] = row0 + item / tile_cols;
+      tc[u] = item % tile_cols;
+      const int col = tc[u] * 128 + lane * 8;
+      in[u] = item < items && row[u] < a.rows && col < a.k;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      if (in[u]) load8(x + (size_t)row[u] * a.k + col, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int item = i0 + u * kHalfWarps + hw;
+      uint2 q;
+      const uint32_t byte = mx_encode8<FMT>(v[u], &q);
+      const uint32_t scales = mx_gather_scales(byte);
+      if (in[u]) {
+        const size_t vec = ((size_t)row[u] * a.k + tc[u] * 128 + lane * 8) / 8;
+        if constexpr (FMT == WQL_MX_FP4)
+          reinterpret_cast<uint32_t*>(a.codes)[vec] = q.x;
+        else
+          reinterpret_cast<uint2*>(a.codes)[vec] = q;
+      }
+      if (lane == 0 && item < items)
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
+                                     mx_scale_at(row[u], tc[u], tile_cols)) = scales;
+    }
+  }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+    mx_dequantize_kernel(const MxDequantizeArgs a, int tile_cols, int rows_per_cta) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  const int row0 = blockIdx.x * rows_per_cta;
+  const int items = min(rows_per_cta, a.rows - row0) * tile_cols;
+  const uint8_t* scales = reinterpret_cast<const uint8_t*>(a.scales);
+  for (int i0 = 0; i0 < items; i0 += kUnroll * kHalfWarps) {
+    uint2 q[kUnroll];
+    uint32_t sw[kUnroll];
+    int row[kUnroll], col[kUnroll];
+    bool in[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int item = i0 + u * kHalfWarps + hw;
+      row[u] = row0 + item / tile_cols;
+      const int tc = item % tile_cols;
+      col[u] = tc * 128 + lane * 8;
+      in[u] = item < items && col[u] < a.k;
+      q[u] = make_uint2(0u, 0u);
+      sw[u] = 0u;
+      if (in[u]) {
+        const size_t vec = ((size_t)row[u] * a.k + col[u]) / 8;
+        if constexpr (FMT == WQL_MX_FP4)
+          q[u].x = __ldg(reinterpret_cast<const uint32_t*>(a.codes) + vec);
+        else
+          q[u] = __ldg(reinterpret_cast<const uint2*>(a.codes) + vec);
+        sw[u] = __ldg(reinterpret_cast<const uint32_t*>(
+            scales + mx_scale_at(row[u], tc, tile_cols)));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!in[u]) continue;
+      const float s = mx_scale_value((sw[u] >> (8 * (lane >> 2))) & 0xFFu);
+      float v[8];
+      if constexpr (FMT == WQL_MX_FP4)
+        mx_values_fp4(q[u].x, v);
+      else
+        mx_values_fp8(q[u], v);
+      T* dst = reinterpret_cast<T*>(a.out) + (size_t)row[u] * a.k + col[u];
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
+      } else {
+        uint4 o;
+        T* h = reinterpret_cast<T*>(&o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = from_f32<T>(v[j] * s);
+        *reinterpret_cast<uint4*>(dst) = o;
+      }
+    }
+  }
+}
+
+// Rows per block: enough blocks for a few per SM, at most 16 rows each.
+int rows_per_cta(int rows) {
+  const int r = rows / (device_sm_count() * 8);
+  return r < 1 ? 1 : r > 16 ? 16 : r;
+}
+
+template <typename T>
+cudaError_t quantize_t(const MxQuantizeArgs& a, cudaStream_t s) {
+  const int tile_cols = (int)mx_tile_cols(a.k);
+  const int padded = (a.rows + kMxTileRows - 1) / kMxTileRows * kMxTileRows;
+  const int rpc = rows_per_cta(padded);
+  const dim3 grid((padded + rpc - 1) / rpc);
+  const cudaError_t e =
+      a.format == WQL_MX_FP4
+          ? launch_pdl(mx_quantize_kernel<T, WQL_MX_FP4>, grid, dim3(kThreads), 0, s, a, tile_cols,
+                       padded, rpc)
+          : launch_pdl(mx_quantize_kernel<T, WQL_MX_FP8>, grid, dim3(kThreads), 0, s, a, tile_cols,
+                       padded, rpc);
+  note_launch();
+  return e;
+}
+
+template <typename T>
+cudaError_t dequantize_t(const MxDequantizeArgs& a, cudaStream_t s) {
+  const int tile_cols = (int)mx_tile_cols(a.k);
+  const int rpc = rows_per_cta(a.rows);
+  const dim3 grid((a.rows + rpc - 1) / rpc);
+  const cudaError_t e =
+      a.format == WQL_MX_FP4
+          ? launch_pdl(mx_dequantize_kernel<T, WQL_MX_FP4>, grid, dim3(kThreads), 0, s, a,
+                       tile_cols, rpc)
+          : launch_pdl(mx_dequantize_kernel<T, WQL_MX_FP8>, grid, dim3(kThreads), 0, s, a,
+                       tile_cols, rpc);
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, cudaStream_t s) {
+  switch (a.x_dtype) {
+    case WQL_F32: return quantize_t<float>(a, s);
+    case WQL_F16: return quantize_t<__half>(a, s);
+    default: return quantize_t<__nv_bfloat16>(a, s);
+  }
+}
+
+cudaError_t launch_mx_dequantize(const MxDequantizeArgs& a, cudaStream_t s) {
+  switch (a.out_dtype) {
+    case WQL_F32: return dequantize_t<float>(a, s);
+    case WQL_F16: return dequantize_t<__half>(a, s);
+    default: return dequantize_t<__nv_bfloat16>(a, s);
+  }
+}
+
+}  // namespace wql

@@ -1,0 +1,257 @@
+// norm.cu -- residual addition and root-mean-square norm in front of the
+// head: h = x + residual, y = h * rsqrt(mean(h^2) + eps) * gamma, written in
+// 16 bits, in e4m3 with a scale per row, or in microscaled codes.
+//
+// HBM-bound: 2 bytes each of x, residual and residual_out and 2, 1 or 17/32
+// bytes of y an element.  One block per row: the row stays in registers
+// between the sum of squares and the output, so every byte moves once.  Sums
+// and the norm are fp32; y is rounded once, to the output.
+#include "mx.cuh"
+
+namespace wql {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kThreadsPerSlot = 256;   // more threads only once a thread holds 64 elements
+
+// Sum or maximum over the block; every thread gets it.
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* red) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    // NaN-keeping maximum of non-negative values: their bits order, NaN on top
+    v = MAX ? __uint_as_float(max(__float_as_uint(v), __float_as_uint(o))) : v + o;
+  }
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  __syncthreads();                       // the buffer of an earlier reduction is free
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    v = MAX ? __uint_as_float(max(__float_as_uint(v), __float_as_uint(o))) : v + o;
+  }
+  return v;
+}
+
+// One group of W consecutive elements: W = 8 as one 16-byte access, else
+// single elements.
+template <typename T, int W>
+__device__ __forceinline__ void load_group(const T* p, float (&v)[W]) {
+  if constexpr (W == 8) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const T* h = reinterpret_cast<const T*>(&a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(h[i]);
+  } else {
+    v[0] = to_f32(*p);
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_group(T* p, const float (&v)[W]) {
+  if constexpr (W == 8) {
+    uint4 a;
+    T* h = reinterpret_cast<T*>(&a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<uint4*>(p) = a;
+  } else {
+    *p = from_f32<T>(v[0]);
+  }
+}
+
+// A thread holds G groups of W elements: group g of the row is thread
+// g % threads, slot g / threads.  W = 8 needs k % 8 == 0 and 16-byte aligned
+// tensors; W = 1 takes any width and alignment.
+template <typename T, int OUT, int W, int G>
+__global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
+    add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float red[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t row = blockIdx.x;
+  const int groups = a.k / W;
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.k;
+  const T* res = a.residual ? reinterpret_cast<const T*>(a.residual) + row * a.k : nullptr;
+  const T* gamma = reinterpret_cast<const T*>(a.gamma);
+  float h[G][W];
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int g = j * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < W; ++i) h[j][i] = 0.f;
+    if (g < groups) load_group<T, W>(x + (size_t)g * W, h[j]);
+  }
+  if (res) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int g = j * blockDim.x + threadIdx.x;
+      float r[W];
+      if (g < groups) {
+        load_group<T, W>(res + (size_t)g * W, r);
+#pragma unroll
+        for (int i = 0; i < W; ++i) h[j][i] += r[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+#pragma unroll
+    for (int i = 0; i < W; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+  // (every thread's loads of the row precede this reduction's barrier and
+  // every store follows it, so out and residual_out may be x or residual;
+  // a one-warp block converges at the shuffles)
+  sum = block_reduce<false>(sum, red);
+  const float scale = rsqrtf(sum / (float)a.k + a.eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int g = j * blockDim.x + threadIdx.x;
+    if (g < groups) {
+      if (a.residual_out)
+        store_group<T, W>(reinterpret_cast<T*>(a.residual_out) + row * a.k + (size_t)g * W, h[j]);
+      float gm[W];
+      load_group<T, W>(gamma + (size_t)g * W, gm);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        h[j][i] = h[j][i] * scale * gm[i];
+        if constexpr (OUT == WQL_NORM_E4M3)
+          amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(h[j][i]) & 0x7FFFFFFFu));
+      }
+    }
+  }
+  if constexpr (OUT == WQL_NORM_SAME) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int g = j * blockDim.x + threadIdx.x;
+      if (g < groups)
+        store_group<T, W>(reinterpret_cast<T*>(a.out) + row * a.k + (size_t)g * W, h[j]);
+    }
+  } else if constexpr (OUT == WQL_NORM_E4M3) {
+    amax = block_reduce<true>(amax, red);
+    // max(), not fmaxf(): a NaN row keeps a NaN scale
+    const float s0 = __fmul_rn(amax, 1.0f / 448.0f);
+    const float s = s0 < 1e-8f ? 1e-8f : s0;
+    if (threadIdx.x == 0) reinterpret_cast<float*>(a.scales)[row] = s;
+    uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.k;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int g = j * blockDim.x + threadIdx.x;
+      if (g >= groups) continue;
+      if constexpr (W == 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(h[j][i], s);
+        *reinterpret_cast<uint2*>(out + (size_t)g * 8) = mx_codes_fp8(v);
+      } else {
+        out[g] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(h[j][0], s), __NV_SATFINITE, __NV_E4M3);
+      }
+    }
+  } else {
+    static_assert(W == 8 || OUT < WQL_NORM_MX_FP8, "microscaled rows are whole 8-element groups");
+    constexpr int FMT = OUT == WQL_NORM_MX_FP4 ? WQL_MX_FP4 : WQL_MX_FP8;
+    const int tile_cols = (a.k + 127) / 128;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      // a half warp holds one tile column (blockDim is a multiple of 32, so
+      // group g is lane g % 32); groups past the row are zeros with scale 0
+      const int g = j * blockDim.x + threadIdx.x;
+      uint2 q;
+      const uint32_t byte = mx_encode8<FMT>(h[j], &q);
+      const uint32_t scales = mx_gather_scales(byte);
+      if (g < groups) {
+        const size_t vec = (size_t)row * groups + g;
+        if constexpr (FMT == WQL_MX_FP4)
+          reinterpret_cast<uint32_t*>(a.out)[vec] = q.x;
+        else
+          reinterpret_cast<uint2*>(a.out)[vec] = q;
+      }
+      if ((threadIdx.x & 15) == 0 && (g >> 4) < tile_cols)
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
+                                     mx_scale_at(row, g >> 4, tile_cols)) = scales;
+    }
+  }
+}
+
+// Scale bytes of the rows past m of the last tile: zero.
+__device__ __forceinline__ void pad_scales(const NormArgs& a, int64_t row) {
+  const int tile_cols = (a.k + 127) / 128;
+  for (int t = threadIdx.x; t < tile_cols; t += blockDim.x)
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
+                                 mx_scale_at(row, t, tile_cols)) = 0u;
+}
+
+__global__ void pad_scales_kernel(const NormArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  pad_scales(a, (int64_t)a.m + blockIdx.x);
+}
+
+template <typename T, int OUT, int W, int G>
+cudaError_t launch_g(const NormArgs& a, int threads, cudaStream_t s) {
+  const cudaError_t e =
+      launch_pdl(add_rmsnorm_kernel<T, OUT, W, G>, dim3((unsigned)a.m), dim3(threads), 0, s, a);
+  note_launch();
+  return e;
+}
+
+template <typename T, int OUT, int W>
+cudaError_t launch_w(const NormArgs& a, cudaStream_t s) {
+  const int groups = a.k / W;
+  int g = 1;
+  while (g < 64 / W && groups > kThreadsPerSlot * g) g *= 2;
+  int threads = ((groups + g - 1) / g + 31) / 32 * 32;
+  if (threads > kMaxThreads) return cudaErrorInvalidConfiguration;
+  if constexpr (W == 8) {
+    switch (g) {
+      case 1: return launch_g<T, OUT, W, 1>(a, threads, s);
+      case 2: return launch_g<T, OUT, W, 2>(a, threads, s);
+      case 4: return launch_g<T, OUT, W, 4>(a, threads, s);
+      default: return launch_g<T, OUT, W, 8>(a, threads, s);
+    }
+  } else {
+    switch (g) {
+      case 1: return launch_g<T, OUT, W, 1>(a, threads, s);
+      case 2: return launch_g<T, OUT, W, 2>(a, threads, s);
+      case 4: return launch_g<T, OUT, W, 4>(a, threads, s);
+      case 8: return launch_g<T, OUT, W, 8>(a, threads, s);
+      case 16: return launch_g<T, OUT, W, 16>(a, threads, s);
+      case 32: return launch_g<T, OUT, W, 32>(a, threads, s);
+      default: return launch_g<T, OUT, W, 64>(a, threads, s);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const NormArgs& a, cudaStream_t s) {
+  auto ok = [](const void* p, size_t al) { return (reinterpret_cast<uintptr_t>(p) % al) == 0; };
+  const bool wide = a.k % 8 == 0 && ok(a.x, 16) && ok(a.residual, 16) && ok(a.gamma, 16) &&
+                    ok(a.residual_out, 16) && ok(a.out, a.out_format == WQL_NORM_E4M3 ? 8 : 16);
+  switch (a.out_format) {
+    case WQL_NORM_SAME:
+      return wide ? launch_w<T, WQL_NORM_SAME, 8>(a, s) : launch_w<T, WQL_NORM_SAME, 1>(a, s);
+    case WQL_NORM_E4M3:
+      return wide ? launch_w<T, WQL_NORM_E4M3, 8>(a, s) : launch_w<T, WQL_NORM_E4M3, 1>(a, s);
+    case WQL_NORM_MX_FP8: return launch_w<T, WQL_NORM_MX_FP8, 8>(a, s);
+    default: return launch_w<T, WQL_NORM_MX_FP4, 8>(a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
+  cudaError_t e = a.dtype == WQL_F16 ? launch_t<__half>(a, s) : launch_t<__nv_bfloat16>(a, s);
+  const int pad = (a.m + kMxTileRows - 1) / kMxTileRows * kMxTileRows - a.m;
+  if (e == cudaSuccess && pad > 0 &&
+      (a.out_format == WQL_NORM_MX_FP8 || a.out_format == WQL_NORM_MX_FP4)) {
+    e = launch_pdl(pad_scales_kernel, dim3((unsigned)pad), dim3(128), 0, s, a);
+    note_launch();
+  }
+  return e;
+}
+
+}  // namespace wql

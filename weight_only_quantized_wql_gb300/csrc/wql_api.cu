@@ -15,6 +15,7 @@
 #include "sm100.cuh"
 #include "wql_common.cuh"
 #include "embed.cuh"
+#include "mx.cuh"
 
 namespace wql {
 
@@ -142,6 +143,18 @@ wql_status check_logits_args(const void* x, int32_t x_dtype, int64_t m, const wq
       !aligned(logits_out, 2) || !aligned(bias, 2))
     return WQL_EUNSUPPORTED;
   *g_out = g;
+  return WQL_OK;
+}
+
+// A microscaled operand: format, sizes, pointers, alignment.
+wql_status check_mx(const wql_mx* a) {
+  if (!a || a->rows < 0 || a->k <= 0 || a->reserved != 0) return WQL_EINVAL;
+  if (a->format != WQL_MX_FP4 && a->format != WQL_MX_FP8) return WQL_EINVAL;
+  if (a->rows > 0 && (!a->codes || !a->scales)) return WQL_EINVAL;
+  if (a->k % kMxBlock != 0 || a->k >= (int64_t(1) << 30) ||
+      a->rows >= (int64_t(1) << 31) - kMxTileRows)
+    return WQL_EUNSUPPORTED;
+  if (!aligned(a->codes, 16) || !aligned(a->scales, 16)) return WQL_EUNSUPPORTED;
   return WQL_OK;
 }
 
@@ -393,6 +406,150 @@ wql_status wql_topk_rescore(const void* x, int32_t x_dtype, int64_t m, const voi
   a.topk_val = topk_val;
   a.logits = logits_inout;
   cudaError_t e = launch_rescore(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+size_t wql_mx_scale_bytes(int64_t rows, int64_t k) {
+  if (rows < 0 || k <= 0) return 0;
+  return (size_t)((rows + kMxTileRows - 1) / kMxTileRows) * (size_t)mx_tile_cols(k) * kMxTileBytes;
+}
+
+wql_status wql_mx_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t k,
+                           int32_t format, void* codes_out, void* scales_out,
+                           cudaStream_t stream) {
+  if (rows < 0 || k <= 0) return WQL_EINVAL;
+  if (format != WQL_MX_FP4 && format != WQL_MX_FP8) return WQL_EINVAL;
+  if (rows > 0 && (!x || !codes_out || !scales_out)) return WQL_EINVAL;
+  if (x_dtype != WQL_F32 && !half_dtype(x_dtype)) return WQL_EUNSUPPORTED;
+  if (k % kMxBlock != 0 || k >= (int64_t(1) << 30) || rows >= (int64_t(1) << 31) - kMxTileRows)
+    return WQL_EUNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(codes_out, 16) || !aligned(scales_out, 16))
+    return WQL_EUNSUPPORTED;
+  if (rows == 0) return WQL_OK;
+  MxQuantizeArgs a{};
+  a.x = x;
+  a.x_dtype = x_dtype;
+  a.rows = (int)rows;
+  a.k = (int)k;
+  a.format = format;
+  a.codes = codes_out;
+  a.scales = scales_out;
+  const cudaError_t e = launch_mx_quantize(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+wql_status wql_mx_dequantize(const wql_mx* a, int32_t out_dtype, void* out, cudaStream_t stream) {
+  const wql_status st = check_mx(a);
+  if (st != WQL_OK) return st;
+  if (a->rows > 0 && !out) return WQL_EINVAL;
+  if (out_dtype != WQL_F32 && !half_dtype(out_dtype)) return WQL_EUNSUPPORTED;
+  if (!aligned(out, 16)) return WQL_EUNSUPPORTED;
+  if (a->rows == 0) return WQL_OK;
+  MxDequantizeArgs d{};
+  d.codes = a->codes;
+  d.scales = a->scales;
+  d.format = a->format;
+  d.rows = (int)a->rows;
+  d.k = (int)a->k;
+  d.out_dtype = out_dtype;
+  d.out = out;
+  const cudaError_t e = launch_mx_dequantize(d, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+wql_status wql_mx_logits(const wql_mx* x, const wql_mx* w, const void* bias, int32_t out_dtype,
+                         void* logits_out, void* workspace, size_t ws_bytes,
+                         cudaStream_t stream) {
+  wql_status st = check_mx(x);
+  if (st == WQL_OK) st = check_mx(w);
+  if (st != WQL_OK) return st;
+  if (x->k != w->k) return WQL_EINVAL;
+  const bool work = x->rows > 0 && w->rows > 0;
+  if (work && !logits_out) return WQL_EINVAL;
+  if (w->format != WQL_MX_FP4) return WQL_EUNSUPPORTED;
+  if (!half_dtype(out_dtype)) return WQL_EUNSUPPORTED;
+  if (!aligned(logits_out, 2) || !aligned(bias, 2)) return WQL_EUNSUPPORTED;
+  if (!work) return WQL_OK;
+  const WorkspaceLayout lay = workspace_layout(x->rows, w->rows, 0);
+  if (workspace && (ws_bytes < lay.total || !aligned(workspace, 256))) return WQL_EWORKSPACE;
+  MxLogitsArgs a{};
+  a.x_codes = x->codes;
+  a.x_scales = x->scales;
+  a.x_format = x->format;
+  a.w_codes = w->codes;
+  a.w_scales = w->scales;
+  a.m = (int)x->rows;
+  a.n = (int)w->rows;
+  a.k = (int)x->k;
+  a.bias = bias;
+  a.out_dtype = out_dtype;
+  a.out = logits_out;
+  if (workspace)
+    a.err = reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(workspace) +
+                                            lay.counter_off) + 1;
+  const cudaError_t e = launch_mx_logits(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+wql_status wql_add_rmsnorm(const void* x, const void* residual, const void* gamma, int32_t dtype,
+                           int64_t m, int64_t k, float eps, int32_t out_format, void* out,
+                           void* scales_out, void* residual_out, cudaStream_t stream) {
+  if (m < 0 || k <= 0 || !(eps >= 0.f)) return WQL_EINVAL;
+  if (out_format < WQL_NORM_SAME || out_format > WQL_NORM_MX_FP4) return WQL_EINVAL;
+  if (m > 0 && (!x || !gamma || !out)) return WQL_EINVAL;
+  if (m > 0 && out_format != WQL_NORM_SAME && !scales_out) return WQL_EINVAL;
+  if (!half_dtype(dtype)) return WQL_EUNSUPPORTED;
+  if (k > 65536 || m >= (int64_t(1) << 31) - kMxTileRows) return WQL_EUNSUPPORTED;
+  const bool mx = out_format == WQL_NORM_MX_FP8 || out_format == WQL_NORM_MX_FP4;
+  if (mx && k % kMxBlock != 0) return WQL_EUNSUPPORTED;
+  const size_t al = mx ? 16 : 2;
+  if (!aligned(x, al) || !aligned(residual, al) || !aligned(gamma, al) ||
+      !aligned(residual_out, al) ||
+      !aligned(out, mx ? 16 : out_format == WQL_NORM_SAME ? 2 : 1) ||
+      !aligned(scales_out, mx ? 16 : 4))
+    return WQL_EUNSUPPORTED;
+  if (m == 0) return WQL_OK;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.dtype = dtype;
+  a.m = (int)m;
+  a.k = (int)k;
+  a.eps = eps;
+  a.out_format = out_format;
+  a.out = out;
+  a.scales = scales_out;
+  a.residual_out = residual_out;
+  const cudaError_t e = launch_add_rmsnorm(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n, const float* u,
+                      const float* temperature, const int32_t* top_k, const float* top_p,
+                      const float* min_p, int32_t* ids_out, float* logp_out,
+                      cudaStream_t stream) {
+  if (m < 0 || n <= 0) return WQL_EINVAL;
+  if (m > 0 && (!logits || !u || !ids_out)) return WQL_EINVAL;
+  if (dtype != WQL_F32 && !half_dtype(dtype)) return WQL_EUNSUPPORTED;
+  if (n > WQL_SAMPLE_MAX_N || m >= (int64_t(1) << 27)) return WQL_EUNSUPPORTED;
+  if (!aligned(logits, 16) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+      !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(ids_out, 4) || !aligned(logp_out, 4))
+    return WQL_EUNSUPPORTED;
+  if (m == 0) return WQL_OK;
+  SampleArgs a{};
+  a.logits = logits;
+  a.dtype = dtype;
+  a.m = (int)m;
+  a.n = (int)n;
+  a.u = u;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.ids = ids_out;
+  a.logp = logp_out;
+  const cudaError_t e = launch_sample(a, stream);
   return e == cudaSuccess ? WQL_OK : cuda_fail(e);
 }
 
