@@ -378,7 +378,7 @@ wql_status wql_add_rmsnorm(const void* x, const void* residual, const void* gamm
                            void* residual_out, cudaStream_t stream);
 
 /* Largest vocabulary of wql_sample (its integer sums stay below 2^53). */
-#define WQL_SAMPLE_MAX_N (1 << 22)
+#define WQL_SAMPLE_MAX_N (1 << 20)
 
 /* Draw one token id per row of logits.  Per row, with l the logits (a NaN
  * counts as -inf), t the temperature and u the given random number:

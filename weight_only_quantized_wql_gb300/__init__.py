@@ -50,7 +50,7 @@ FMT_SYM, FMT_E4M3, FMT_ASYM = 0, 1, 2    # wql_format
 WEIGHT_STATIC = 0x100                    # flag ORed into the format field
 MX_FP4, MX_FP8 = 0, 1                    # wql_mx_format
 NORM_SAME, NORM_E4M3, NORM_MX_FP8, NORM_MX_FP4 = 0, 1, 2, 3    # wql_norm_out
-SAMPLE_MAX_N = 1 << 22
+SAMPLE_MAX_N = 1 << 20
 MAX_TOPK = 16
 MAX_CTAS = 1024
 _DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
