@@ -3,6 +3,7 @@
 // C-ABI layer calls.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -122,6 +123,13 @@ __device__ __forceinline__ uint32_t mx_gather_scales(uint32_t byte) {
   for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xFFFFFFFFu, byte, base + 4 * b) << (8 * b);
   return w;
 }
+
+// Tensor map (host) of a row-major [rows, cols] matrix of packed 4-bit codes
+// whose boxes, 128 columns x box_rows, land in shared memory with 16 codes (8
+// bytes) at the start of every 16-byte unit, rows of 128 bytes, 128B-swizzled.
+// cols % 128 == 0, base 32-byte aligned.
+cudaError_t make_tmap_e2m1_spread(CUtensorMap* map, const void* base, uint64_t cols,
+                                  uint64_t rows, uint32_t box_rows);
 
 struct MxQuantizeArgs {
   const void* x;

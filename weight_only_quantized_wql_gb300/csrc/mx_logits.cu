@@ -40,14 +40,17 @@ constexpr int kMaxCopyDepth = 3;                   // stages of copies in flight
 constexpr int kMaxStages = 8, kMinStages = 2;
 constexpr uint32_t kErrWait = 8u;                  // error word: a wait ran out
 
-template <int XFMT> struct Kind {
+// COPY: the weight by cp.async (e2m1 x e4m3 only), else by TMA.
+template <int XFMT, bool COPY> struct Kind {
   static constexpr bool kFp8 = XFMT == WQL_MX_FP8;
   static constexpr int kBlocks = kFp8 ? 2 : 1;          // 128-byte blocks per row and stage
   static constexpr int kMmaCols = kFp8 ? 32 : 64;
   static constexpr int kMmaPerStage = kStageCols / kMmaCols;
   static constexpr int kMmaPerTile = 128 / kMmaCols;    // per scale tile of 128 columns
   static constexpr int kSlice = kFp8 ? 128 : 256;       // most tokens at a time
-  static constexpr int kWarps = kCopyWarp0 + (kFp8 ? kCopyWarps : 0);
+  // bytes a 128-row block of the weight counts on a barrier: the codes themselves
+  static constexpr int kWeightTx = kFp8 ? kTileRows * 64 : kBlockBytes;
+  static constexpr int kWarps = kCopyWarp0 + (COPY ? kCopyWarps : 0);
 };
 
 struct MxParams {
@@ -153,11 +156,11 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int XFMT, typename OT>
-__global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
+template <int XFMT, bool COPY, typename OT>
+__global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
     mx_logits_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
                      const MxParams p) {
-  using K = Kind<XFMT>;
+  using K = Kind<XFMT, COPY>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ring; ++s) {
-      mbar_init(&full[s], 1 + (K::kFp8 ? kCopyWarps : 0));
+      mbar_init(&full[s], 1 + (COPY ? kCopyWarps : 0));
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
     // ---------------- TMA: X, scales, and (e2m1 x e2m1) the weight ----------------
     if (lane == 0) {
       prefetch_tmap(&tx);
-      if (!K::kFp8) prefetch_tmap(&tw);
+      if (!COPY) prefetch_tmap(&tw);
       const uint8_t* wsc = reinterpret_cast<const uint8_t*>(a.w_scales);
       const uint8_t* xsc = reinterpret_cast<const uint8_t*>(a.x_scales);
       const int xt = (tokens + 127) / 128;           // this slice's token scale tiles
@@ -226,9 +229,12 @@ __global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
           const int kt = c * 2, nkt = min(2, p.tile_cols - kt);    // scale tiles of this stage
           const uint32_t sbytes = (uint32_t)(nkt * kMxTileBytes);
           const uint32_t bytes = (uint32_t)(K::kBlocks * p.npad * 128) + sbytes * (1 + xt) +
-                                 (K::kFp8 ? 0u : (uint32_t)kBlockBytes);
+                                 (COPY ? 0u : (uint32_t)(K::kBlocks * K::kWeightTx));
           mbar_arrive_expect_tx(&full[slot], bytes);
-          if (!K::kFp8) tma_load_2d(st, &tw, c * 32, t * kTileRows, &full[slot]);
+          if (!COPY)
+            for (int b = 0; b < K::kBlocks; ++b)      // x in map elements: words, or codes
+              tma_load_2d(st + b * kBlockBytes, &tw, (c * K::kBlocks + b) * (K::kFp8 ? 128 : 32),
+                          t * kTileRows, &full[slot]);
           for (int b = 0; b < K::kBlocks; ++b)
             tma_load_2d(st + p.off_x + b * p.npad * 128, &tx, (c * K::kBlocks + b) * 32,
                         slice * K::kSlice, &full[slot]);
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
       if (lane == 0) mbar_arrive(&acc_empty[acc]);
       if (++acc == p.acc_bufs) { acc = 0; acc_phase ^= 1u; }
     }
-  } else {
+  } else if constexpr (COPY) {
     // ---------------- the weight's codes, 8 bytes to each 16-byte unit ----------------
     const int id = (warp - kCopyWarp0) * 32 + lane;          // 0..127
     const int piece = id & 15, r0 = id >> 4;                 // 16 pieces of 16 codes; rows r0 + 8 i
@@ -392,9 +398,9 @@ __global__ void __launch_bounds__(Kind<XFMT>::kWarps * 32, 1)
   if (threadIdx.x == 0 && *failed != 0u && a.err) atomicOr(a.err, kErrWait);
 }
 
-template <int XFMT, typename OT>
+template <int XFMT, bool COPY, typename OT>
 cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
-  using K = Kind<XFMT>;
+  using K = Kind<XFMT, COPY>;
   MxParams p{};
   p.a = a;
   p.wait_budget = diag_wait_budget();
@@ -423,13 +429,17 @@ cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
 
   CUtensorMap tw, tx;
   const uint64_t wrow = (uint64_t)a.k / 2, xrow = K::kFp8 ? (uint64_t)a.k : (uint64_t)a.k / 2;
-  cudaError_t e = make_tmap_2d(&tw, a.w_codes, 4, wrow / 4, (uint64_t)a.n, wrow, 32, kTileRows,
-                               Swizzle::k128B);
+  cudaError_t e = cudaSuccess;
+  if (K::kFp8 && !COPY)
+    e = make_tmap_e2m1_spread(&tw, a.w_codes, (uint64_t)a.k, (uint64_t)a.n, kTileRows);
+  else
+    e = make_tmap_2d(&tw, a.w_codes, 4, wrow / 4, (uint64_t)a.n, wrow, 32, kTileRows,
+                     Swizzle::k128B);
   if (e != cudaSuccess) return e;
   e = make_tmap_2d(&tx, a.x_codes, 4, xrow / 4, (uint64_t)a.m, xrow, 32, (uint32_t)p.npad,
                    Swizzle::k128B);
   if (e != cudaSuccess) return e;
-  auto kern = mx_logits_kernel<XFMT, OT>;
+  auto kern = mx_logits_kernel<XFMT, COPY, OT>;
   static size_t configured = 0;
   if (smem > configured) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -447,11 +457,17 @@ cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mx_logits(const MxLogitsArgs& a, cudaStream_t s) {
+  const bool f16 = a.out_dtype == WQL_F16;
   if (a.x_format == WQL_MX_FP4)
-    return a.out_dtype == WQL_F16 ? launch_t<WQL_MX_FP4, __half>(a, s)
-                                  : launch_t<WQL_MX_FP4, __nv_bfloat16>(a, s);
-  return a.out_dtype == WQL_F16 ? launch_t<WQL_MX_FP8, __half>(a, s)
-                                : launch_t<WQL_MX_FP8, __nv_bfloat16>(a, s);
+    return f16 ? launch_t<WQL_MX_FP4, false, __half>(a, s)
+               : launch_t<WQL_MX_FP4, false, __nv_bfloat16>(a, s);
+  // TMA spreads e2m1 codes over 16-byte units itself, for whole 128-column
+  // blocks of 32-byte aligned rows
+  if (a.k % 128 == 0 && reinterpret_cast<uintptr_t>(a.w_codes) % 32 == 0)
+    return f16 ? launch_t<WQL_MX_FP8, false, __half>(a, s)
+               : launch_t<WQL_MX_FP8, false, __nv_bfloat16>(a, s);
+  return f16 ? launch_t<WQL_MX_FP8, true, __half>(a, s)
+             : launch_t<WQL_MX_FP8, true, __nv_bfloat16>(a, s);
 }
 
 }  // namespace wql

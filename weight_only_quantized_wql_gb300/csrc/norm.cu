@@ -63,6 +63,14 @@ __device__ __forceinline__ void store_group(T* p, const float (&v)[W]) {
   }
 }
 
+// Scale bytes of a row past m in the last tile: zero.
+__device__ __forceinline__ void pad_scales(const NormArgs& a, int64_t row) {
+  const int tile_cols = (a.k + 127) / 128;
+  for (int t = threadIdx.x; t < tile_cols; t += blockDim.x)
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
+                                 mx_scale_at(row, t, tile_cols)) = 0u;
+}
+
 // A thread holds G groups of W elements: group g of the row is thread
 // g % threads, slot g / threads.  W = 8 needs k % 8 == 0 and 16-byte aligned
 // tensors; W = 1 takes any width and alignment.
@@ -73,6 +81,12 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row = blockIdx.x;
+  if constexpr (OUT >= WQL_NORM_MX_FP8) {
+    if (row >= a.m) {
+      pad_scales(a, row);
+      return;
+    }
+  }
   const int groups = a.k / W;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.k;
   const T* res = a.residual ? reinterpret_cast<const T*>(a.residual) + row * a.k : nullptr;
@@ -177,24 +191,12 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
   }
 }
 
-// Scale bytes of the rows past m of the last tile: zero.
-__device__ __forceinline__ void pad_scales(const NormArgs& a, int64_t row) {
-  const int tile_cols = (a.k + 127) / 128;
-  for (int t = threadIdx.x; t < tile_cols; t += blockDim.x)
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
-                                 mx_scale_at(row, t, tile_cols)) = 0u;
-}
-
-__global__ void pad_scales_kernel(const NormArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  pad_scales(a, (int64_t)a.m + blockIdx.x);
-}
-
 template <typename T, int OUT, int W, int G>
 cudaError_t launch_g(const NormArgs& a, int threads, cudaStream_t s) {
+  const int rows = OUT >= WQL_NORM_MX_FP8
+                       ? (a.m + kMxTileRows - 1) / kMxTileRows * kMxTileRows : a.m;
   const cudaError_t e =
-      launch_pdl(add_rmsnorm_kernel<T, OUT, W, G>, dim3((unsigned)a.m), dim3(threads), 0, s, a);
+      launch_pdl(add_rmsnorm_kernel<T, OUT, W, G>, dim3((unsigned)rows), dim3(threads), 0, s, a);
   note_launch();
   return e;
 }
@@ -244,14 +246,7 @@ cudaError_t launch_t(const NormArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
-  cudaError_t e = a.dtype == WQL_F16 ? launch_t<__half>(a, s) : launch_t<__nv_bfloat16>(a, s);
-  const int pad = (a.m + kMxTileRows - 1) / kMxTileRows * kMxTileRows - a.m;
-  if (e == cudaSuccess && pad > 0 &&
-      (a.out_format == WQL_NORM_MX_FP8 || a.out_format == WQL_NORM_MX_FP4)) {
-    e = launch_pdl(pad_scales_kernel, dim3((unsigned)pad), dim3(128), 0, s, a);
-    note_launch();
-  }
-  return e;
+  return a.dtype == WQL_F16 ? launch_t<__half>(a, s) : launch_t<__nv_bfloat16>(a, s);
 }
 
 }  // namespace wql
