@@ -299,7 +299,8 @@ typedef enum wql_mx_format {
  *           ceil(k/128)], 512 bytes each: row r, block b of a tile at byte
  *           16 * (r % 32) + 4 * (r / 32) + b.  This is the order in which the
  *           tensor cores take them.  Bytes past the last row or block are 0.
- * Requirements: k % 32 == 0; codes and scales 16-byte aligned; rows < 2^31. */
+ * Requirements: k % 32 == 0, k <= 2^20; codes and scales 16-byte aligned;
+ * rows < 2^31 - 128. */
 typedef struct wql_mx {
   int32_t format;      /* wql_mx_format */
   int32_t reserved;    /* 0 */
@@ -362,8 +363,8 @@ typedef enum wql_norm_out {
  *   y = h * rsqrt(mean_k(h^2) + eps) * gamma,
  * and y is written as out_format says, rounded once:
  *   E4M3       s = max(max_k |y| *f32 fl32(1/448), 1e-8f),
- *              code = RN_e4m3(clamp(y /f32 s, -448, 448)); a NaN in a row
- *              makes its scale NaN
+ *              code = RN_e4m3(clamp(y *f32 (1 /f32 s), -448, 448)); a NaN in
+ *              a row makes its scale NaN
  *   MX_FP8/4   as wql_mx_quantize
  *   x, residual   device [m, k] of dtype (F16 or BF16)
  *   gamma         device [k] of dtype

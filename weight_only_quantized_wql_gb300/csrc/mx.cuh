@@ -14,6 +14,7 @@ namespace wql {
 constexpr int kMxBlock = 32;        // columns per scale
 constexpr int kMxTileRows = 128;    // a scale tile: 128 rows x 4 blocks, 512 bytes
 constexpr int kMxTileBytes = 512;
+constexpr int kMxMaxK = 1 << 20;
 
 __host__ __device__ __forceinline__ int64_t mx_tile_cols(int64_t k) { return (k + 127) / 128; }
 
@@ -91,13 +92,20 @@ __device__ __forceinline__ void mx_values_fp8(uint2 w, float (&v)[8]) {
   }
 }
 
+// max(|a|, |b|), NaN if either is.
+__device__ __forceinline__ float mx_max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 // A group of four consecutive lanes holds a block, eight values each: encode
 // this lane's eight (`x` in fp32) and return the block's scale byte.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint2* codes) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  const float m = mx_max_abs(mx_max_abs(mx_max_abs(x[0], x[1]), mx_max_abs(x[2], x[3])),
+                             mx_max_abs(mx_max_abs(x[4], x[5]), mx_max_abs(x[6], x[7])));
+  uint32_t am = __float_as_uint(m) & 0x7FFFFFFFu;
   am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
   am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
   const uint32_t byte = mx_scale_byte<FMT>(am);
@@ -114,22 +122,14 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint2* codes
   return byte;
 }
 
-// The four blocks of a half warp (lanes 0..15 or 16..31, one scale tile
-// column): their bytes as one word, valid in every lane.
-__device__ __forceinline__ uint32_t mx_gather_scales(uint32_t byte) {
-  const int base = threadIdx.x & 16;
-  uint32_t w = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xFFFFFFFFu, byte, base + 4 * b) << (8 * b);
-  return w;
-}
-
-// Tensor map (host) of a row-major [rows, cols] matrix of packed 4-bit codes
-// whose boxes, 128 columns x box_rows, land in shared memory with 16 codes (8
-// bytes) at the start of every 16-byte unit, rows of 128 bytes, 128B-swizzled.
-// cols % 128 == 0, base 32-byte aligned.
-cudaError_t make_tmap_e2m1_spread(CUtensorMap* map, const void* base, uint64_t cols,
-                                  uint64_t rows, uint32_t box_rows);
+// Tensor map (host) of a row-major matrix of rows of row_bytes, seen as
+// [blocks of columns][rows][one block], whose boxes of box_blocks x box_rows
+// blocks land in shared memory as rows of 128 bytes, 128B-swizzled, block after
+// block.  A block is 128 bytes of a row, or (spread) 64 bytes, 128 packed 4-bit
+// codes, of which 16 (8 bytes) land at the start of every 16-byte unit.
+// row_bytes: whole blocks; base 16-byte (spread: 32-byte) aligned.
+cudaError_t make_tmap_blocks(CUtensorMap* map, bool spread, const void* base, uint64_t row_bytes,
+                             uint64_t rows, uint32_t box_rows, uint32_t box_blocks);
 
 struct MxQuantizeArgs {
   const void* x;

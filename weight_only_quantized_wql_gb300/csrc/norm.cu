@@ -12,7 +12,6 @@ namespace wql {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kThreadsPerSlot = 256;   // more threads only once a thread holds 64 elements
 
 // Sum or maximum over the block; every thread gets it.
 template <bool MAX>
@@ -35,6 +34,13 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
     v = MAX ? __uint_as_float(max(__float_as_uint(v), __float_as_uint(o))) : v + o;
   }
   return v;
+}
+
+// max(a, |v|) for a >= 0, NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(v)));
+  return r;
 }
 
 // One group of W consecutive elements: W = 8 as one 16-byte access, else
@@ -75,8 +81,7 @@ __device__ __forceinline__ void pad_scales(const NormArgs& a, int64_t row) {
 // g % threads, slot g / threads.  W = 8 needs k % 8 == 0 and 16-byte aligned
 // tensors; W = 1 takes any width and alignment.
 template <typename T, int OUT, int W, int G>
-__global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
-    add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float red[32];
   griddep_launch_dependents();
   griddep_wait();
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
       for (int i = 0; i < W; ++i) {
         h[j][i] = h[j][i] * scale * gm[i];
         if constexpr (OUT == WQL_NORM_E4M3)
-          amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(h[j][i]) & 0x7FFFFFFFu));
+          amax = max_abs(amax, h[j][i]);
       }
     }
   }
@@ -147,9 +152,9 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
     }
   } else if constexpr (OUT == WQL_NORM_E4M3) {
     amax = block_reduce<true>(amax, red);
-    // max(), not fmaxf(): a NaN row keeps a NaN scale
     const float s0 = __fmul_rn(amax, 1.0f / 448.0f);
-    const float s = s0 < 1e-8f ? 1e-8f : s0;
+    const float s = s0 < 1e-8f ? 1e-8f : s0;          // (a NaN stays)
+    const float inv = __fdiv_rn(1.f, s);
     if (threadIdx.x == 0) reinterpret_cast<float*>(a.scales)[row] = s;
     uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.k;
 #pragma unroll
@@ -159,10 +164,10 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
       if constexpr (W == 8) {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(h[j][i], s);
+        for (int i = 0; i < 8; ++i) v[i] = h[j][i] * inv;
         *reinterpret_cast<uint2*>(out + (size_t)g * 8) = mx_codes_fp8(v);
       } else {
-        out[g] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(h[j][0], s), __NV_SATFINITE, __NV_E4M3);
+        out[g] = (uint8_t)__nv_cvt_float_to_fp8(h[j][0] * inv, __NV_SATFINITE, __NV_E4M3);
       }
     }
   } else {
@@ -171,12 +176,12 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
     const int tile_cols = (a.k + 127) / 128;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      // a half warp holds one tile column (blockDim is a multiple of 32, so
-      // group g is lane g % 32); groups past the row are zeros with scale 0
+      // four lanes hold a block, a half warp one tile column (blockDim is a
+      // multiple of 32, so group g is lane g % 32); groups past the row are
+      // zeros with scale 0
       const int g = j * blockDim.x + threadIdx.x;
       uint2 q;
       const uint32_t byte = mx_encode8<FMT>(h[j], &q);
-      const uint32_t scales = mx_gather_scales(byte);
       if (g < groups) {
         const size_t vec = (size_t)row * groups + g;
         if constexpr (FMT == WQL_MX_FP4)
@@ -184,9 +189,9 @@ __global__ void __launch_bounds__(G == 64 / W ? kMaxThreads : kThreadsPerSlot)
         else
           reinterpret_cast<uint2*>(a.out)[vec] = q;
       }
-      if ((threadIdx.x & 15) == 0 && (g >> 4) < tile_cols)
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.scales) +
-                                     mx_scale_at(row, g >> 4, tile_cols)) = scales;
+      if ((threadIdx.x & 3) == 0 && (g >> 4) < tile_cols)
+        reinterpret_cast<uint8_t*>(a.scales)[mx_scale_at(row, g >> 4, tile_cols) +
+                                             ((g >> 2) & 3)] = (uint8_t)byte;
     }
   }
 }
@@ -203,9 +208,13 @@ cudaError_t launch_g(const NormArgs& a, int threads, cudaStream_t s) {
 
 template <typename T, int OUT, int W>
 cudaError_t launch_w(const NormArgs& a, cudaStream_t s) {
+  // Threads per row: few rows want all their loads out at once (1 x 5120: 640
+  // threads, one group each), many rows small blocks with several loads per
+  // thread; single elements always more threads.
   const int groups = a.k / W;
+  const int most = a.m < 2 * device_sm_count() ? kMaxThreads : W == 1 ? 512 : 256;
   int g = 1;
-  while (g < 64 / W && groups > kThreadsPerSlot * g) g *= 2;
+  while (g < 64 / W && groups > most * g) g *= 2;
   int threads = ((groups + g - 1) / g + 31) / 32 * 32;
   if (threads > kMaxThreads) return cudaErrorInvalidConfiguration;
   if constexpr (W == 8) {

@@ -52,19 +52,20 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uin
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_e2m1_spread(CUtensorMap* map, const void* base, uint64_t cols,
-                                  uint64_t rows, uint32_t box_rows) {
+cudaError_t make_tmap_blocks(CUtensorMap* map, bool spread, const void* base, uint64_t row_bytes,
+                             uint64_t rows, uint32_t box_rows, uint32_t box_blocks) {
   std::call_once(g_encode_once, resolve_encoder);
   if (!g_encode) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols / 2};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2,
-                              const_cast<void*>(base), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const uint64_t block = spread ? 64 : 128;
+  const cuuint64_t dims[3] = {spread ? 128u : 32u, rows, row_bytes / block};
+  const cuuint64_t strides[2] = {row_bytes, block};
+  const cuuint32_t box[3] = {spread ? 128u : 32u, box_rows, box_blocks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(
+      map, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3,
+      const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -167,7 +168,7 @@ wql_status check_mx(const wql_mx* a) {
   if (!a || a->rows < 0 || a->k <= 0 || a->reserved != 0) return WQL_EINVAL;
   if (a->format != WQL_MX_FP4 && a->format != WQL_MX_FP8) return WQL_EINVAL;
   if (a->rows > 0 && (!a->codes || !a->scales)) return WQL_EINVAL;
-  if (a->k % kMxBlock != 0 || a->k >= (int64_t(1) << 30) ||
+  if (a->k % kMxBlock != 0 || a->k > kMxMaxK ||
       a->rows >= (int64_t(1) << 31) - kMxTileRows)
     return WQL_EUNSUPPORTED;
   if (!aligned(a->codes, 16) || !aligned(a->scales, 16)) return WQL_EUNSUPPORTED;
@@ -437,7 +438,7 @@ wql_status wql_mx_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t
   if (format != WQL_MX_FP4 && format != WQL_MX_FP8) return WQL_EINVAL;
   if (rows > 0 && (!x || !codes_out || !scales_out)) return WQL_EINVAL;
   if (x_dtype != WQL_F32 && !half_dtype(x_dtype)) return WQL_EUNSUPPORTED;
-  if (k % kMxBlock != 0 || k >= (int64_t(1) << 30) || rows >= (int64_t(1) << 31) - kMxTileRows)
+  if (k % kMxBlock != 0 || k > kMxMaxK || rows >= (int64_t(1) << 31) - kMxTileRows)
     return WQL_EUNSUPPORTED;
   if (!aligned(x, 16) || !aligned(codes_out, 16) || !aligned(scales_out, 16))
     return WQL_EUNSUPPORTED;
