@@ -62,6 +62,7 @@ constexpr uint32_t kErrWait = 8u;                  // error word: a wait ran out
 // COPY: the weight by cp.async (e2m1 x e4m3 only), else by TMA.
 template <int XFMT, bool COPY> struct Kind {
   static constexpr bool kFp8 = XFMT == WQL_MX_FP8;
+  static constexpr bool kCopy = COPY;
   static constexpr int kBlocks = kFp8 ? 2 : 1;          // 128-byte blocks per row and stage
   static constexpr int kMmaCols = kFp8 ? 32 : 64;
   static constexpr int kMmas = kCols / kMmaCols;        // products of a stage
@@ -548,7 +549,10 @@ constexpr uint32_t rup1k(uint32_t v) { return (v + 1023u) & ~1023u; }
 // than kMinStages stages fit.
 template <typename K> bool plan(MxParams& p, int most) {
   const int m = p.a.m;
-  const uint32_t room = 227u * 1024u - 1024u - kBarBytes - (uint32_t)(2 * p.out_bufs * kOutBytes);
+  // cp.async fetches through the L1 that shares the SM's memory: with 227 KB
+  // taken, 64 tokens on a 151936 x 992 head took 43.0 us, with 192 KB 30.9
+  const uint32_t room = (K::kCopy ? 192u : 227u) * 1024u - 1024u - kBarBytes -
+                        (uint32_t)(2 * p.out_bufs * kOutBytes);
   auto lay = [&](int slice, bool resident) {
     p.slice = slice;
     p.slices = (m + slice - 1) / slice;
@@ -592,9 +596,10 @@ cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
   p.tiles = (a.n + kTileRows - 1) / kTileRows;
   p.tile_cols = (int)mx_tile_cols(a.k);
   p.stages_k = (a.k + kCols - 1) / kCols;
-  // few tokens: 64-byte stores straight from registers; up to two groups of 16,
-  // one block per group and tile, need one buffer each
-  p.tma_store = a.m > 8 && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  // few tokens: 64-byte stores straight from registers (copying the weight, they
+  // leave room for a fifth stage); up to two groups of 16, one block per group
+  // and tile, need one buffer each
+  p.tma_store = a.m > (COPY ? 32 : 8) && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   p.out_bufs = !p.tma_store ? 0 : a.m <= 2 * kOutTokens ? 1 : 2;
   if (!plan<K>(p, K::kFp8 ? 128 : 256)) return cudaErrorInvalidConfiguration;
   const size_t smem = p.off_bar + kBarBytes + 1024;
