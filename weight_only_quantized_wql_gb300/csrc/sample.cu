@@ -7,30 +7,37 @@
 // filters come down to one cut, the rank key of the last kept token:
 // (order-preserving bits of the logit, inverted index).
 //
-// One cluster of 1 to 8 blocks per row, each over a contiguous slice:
+// One cluster of 1 to 8 blocks per row, each over a contiguous slice, which
+// stays in shared memory when it fits (76 KB, so that two blocks share an SM
+// and one's copies run under the other's passes):
 //  * the maximum (and those of four shares of each thread's elements);
-//  * top-k up to 768: a bound that about k logits reach, from a histogram of
+//  * top-k up to 512: a bound that about k logits reach, from a histogram of
 //    the share maxima (k values at least as large exist if k maxima do); one
 //    pass gathers the logits above it; the first block ranks that list,
 //    applies the filters by prefix sums and draws;
-//  * a nucleus, or a larger top-k: a histogram of the weights (counts) over
-//    quarter octaves below the maximum finds the one that holds the cut, a
-//    second pass gathers its tokens, the first block ranks them; while they do
-//    not fit the list, further histograms over seven bits of the rank key at a
-//    time narrow them.  The draw then runs over the row by index, as it does
-//    when temperature or min-p alone is on: sums per stretch of the row, then
-//    a walk through the one stretch that holds the draw.
+//  * a nucleus: a histogram of the weights over quarter octaves below the
+//    maximum finds the one that holds the cut; a second pass sums the weights
+//    above it per stretch of the row and gathers its own tokens, which the
+//    first block ranks to find the cut; their kept weights join the stretches'
+//    sums, and the draw walks the one stretch that holds it;
+//  * a larger top-k, or more open tokens than the list holds: histograms of
+//    counts or weights, first over quarter octaves, then over seven bits of the
+//    rank key at a time, until the open tokens fit; then, as when temperature
+//    or min-p alone is on, one pass for the stretches' sums and the walk.
 //
-// What bounds it: two passes at least over a row that the second time comes
-// from L2, and per weight some ten instructions, among them an exponential
-// and a conversion on the slow unit.  The loops over a row are kept short (one
-// 16-byte piece a turn, the next three in flight): unrolled by four they were
-// bound by instruction fetches (64 x 248320 fp32, temperature alone: 44.7 us).  Histograms keep 32 copies, one per lane, so that a
-// warp's additions never meet in a bank; a copy's sums (16 low and 15 high bits
-// of the weights apart) stay below 2^32 for 2^20 tokens.
+// What bounds it: per weight some ten to twenty instructions, among them an
+// exponential and a conversion on the slow unit, and two or three passes.  The
+// loops over a row are kept short (one 16-byte piece a turn): unrolled by four
+// they were bound by instruction fetches (64 x 248320 fp32, temperature alone:
+// 44.7 us).  Histograms keep 16 copies, one per lane and its half warp's
+// partner, so that a warp's additions hardly meet in a bank; a copy's sums (16
+// low and 15 high bits of the weights apart) stay below 2^32 for 2^20 tokens.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "mx.cuh"
+#include "sm100.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -41,38 +48,52 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 2048;          // tokens the list holds
+constexpr int kList = 2048;          // tokens the joined list holds
+constexpr int kLocal = 1024;         // a block's own list, in a cluster
 constexpr int kBins = 128;
-constexpr int kShares = 4;           // maxima kept per thread; loads in flight per thread
-constexpr int kSegs = 32;            // stretches of a warp's part of the row
+constexpr int kCopies = 16;          // of a histogram
+constexpr int kShares = 4;           // maxima kept per thread
+constexpr int kSegs = 16;            // stretches of a warp's part of the row
+constexpr int kChunks = 4;           // copies that bring a slice in, four warps' parts each
 constexpr int kMaxCluster = 8;
-constexpr int kMaxListK = 768;       // largest top-k that goes by a bound and a list
+constexpr int kMaxListK = 512;       // largest top-k that goes by a bound and a list
 constexpr int kCountRank = 128;      // lists up to this long are ranked by counting
 constexpr int kIndexBits = 20;
+constexpr int kHeldBytes = 76 * 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 static_assert(WQL_SAMPLE_MAX_N == 1 << kIndexBits, "rank keys hold an index");
 
-struct Shared {
-  uint32_t low[kBins][32];           // sums of weights' low 16 bits, by lane
-  uint32_t high[kBins][32];          // and of the bits above
-  uint32_t count[kBins][32];
-  u64 list[kList];
-  uint32_t weight[kList];
+struct alignas(16) Shared {
+  u64 list[kLocal];
   u64 seg[kWarps][kSegs];
   u64 red[kWarps];
   float redf[kWarps];
+  uint64_t bars[kChunks];
   // read by the other blocks of the cluster
   u64 bin_mass[kBins];
   uint32_t bin_count[kBins];
   float max;
+  int failed;                          // a wait for this block's copies ran out
   u64 sum;
   uint32_t listed;
-  u64 cut;                           // of the first block
-  int done;
+  u64 cut;                             // of the first block
   // block-wide results
   int digit;
   u64 before_count, before_mass;
+  // histograms; once they are folded, the joined list takes their place: kList
+  // keys, then their weights
+  struct alignas(16) {
+    uint32_t low[kBins][kCopies];      // sums of weights' low 16 bits
+    uint32_t high[kBins][kCopies];     // and of the bits above
+    uint32_t count[kBins][kCopies];
+  } hist;
 };
+static_assert(sizeof(Shared::hist) == kList * 12, "the joined list takes the histograms' place");
+
+__device__ __forceinline__ u64* keys(Shared& sh) { return reinterpret_cast<u64*>(&sh.hist); }
+__device__ __forceinline__ uint32_t* weights(Shared& sh) {
+  return reinterpret_cast<uint32_t*>(keys(sh) + kList);
+}
 
 __device__ __forceinline__ uint32_t logit_key(float l) {
   const uint32_t b = __float_as_uint(l + 0.f);        // -0 ranks as +0
@@ -95,10 +116,10 @@ struct Row {
   float top;       // largest logit
   float c;         // log2e / temperature
   float min_p;     // 0: off
-  // log2 of a token's weight over the likeliest's (NaN for a NaN; top is
-  // finite here, and so is c)
+  // log2 of a token's weight over the likeliest's, not below -1000, which a
+  // NaN becomes too (top and c are finite here)
   __device__ __forceinline__ float depth(float l) const {
-    return __fmul_rn(__fsub_rn(l, top), c);
+    return fmaxf(__fmul_rn(__fsub_rn(l, top), c), -1000.f);
   }
   // 2^x; the same bits as exp2f() from -126 up, and W = 0 below -31 anyway
   static __device__ __forceinline__ float e(float x) {
@@ -106,34 +127,64 @@ struct Row {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
   }
-  // (a NaN converts to 0)
   static __device__ __forceinline__ uint32_t weight(float e) {
     return __float2uint_rz(e * 2147483648.f);
   }
+  // The same in two halves without the conversion, which shares the slow unit
+  // with the exponential: floats 2^23 + W / 2^16 and 2^23 + W % 2^16 (each
+  // product is exact, each sum truncates), whose bits are kOne + the half.
+  static constexpr uint32_t kOne = 0x4B000000u;
+  static __device__ __forceinline__ void halves(float e, uint32_t* high, uint32_t* low) {
+    const float h = __fmaf_rz(e, 32768.f, 8388608.f);
+    const float rest = __fmaf_rn(__fsub_rn(h, 8388608.f), -1.f / 32768.f, e);
+    *high = __float_as_uint(h);
+    *low = __float_as_uint(__fmaf_rz(rest, 2147483648.f, 8388608.f));
+  }
   // quarter octaves below the maximum, rounded to the nearest: never
   // decreasing with the logit's rank, at most 124 for a token with a weight
+  static __device__ __forceinline__ uint32_t bin_if_weight(float x) {
+    return __float_as_uint(fmaf(x, -4.f, 8388608.f)) - 0x4B000000u;
+  }
   static __device__ __forceinline__ int bin(float x) {
-    return (int)min(__float_as_uint(fmaf(x, -4.f, 8388608.f)) - 0x4B000000u,
-                    (uint32_t)(kBins - 1));
+    return (int)min(bin_if_weight(x), (uint32_t)(kBins - 1));
   }
 };
 
 // A row of logits in 16-byte pieces on 16-byte addresses: piece q holds
-// elements q*V - mis .. + V-1; those outside the row read as -inf.
-template <typename T> struct Pieces {
+// elements q*V - mis .. + V-1; those outside the row read as -inf.  HELD: this
+// block's pieces, from s0 on, are read from shared memory; otherwise only the
+// row's first and last one, which may reach outside it.
+template <typename T, bool HELD> struct Pieces {
   static constexpr int V = 16 / (int)sizeof(T);
   const T* base;       // 16-byte aligned, mis elements before the row
-  int mis, n, pieces;
-  __device__ __forceinline__ Pieces(const T* row, int n_) : n(n_) {
+  uint4* held;
+  int mis, n, pieces, s0;
+  __device__ __forceinline__ Pieces(const T* row, int n_, uint8_t* smem) : n(n_) {
     mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     base = row - mis;
     pieces = (n + mis + V - 1) / V;
+    held = reinterpret_cast<uint4*>(smem);
+    s0 = 0;
+  }
+  // first piece of a warp's part
+  __device__ __forceinline__ int first(int part, int parts) const {
+    return (int)((long long)pieces * part / parts);
+  }
+  // the part that piece q lies in: the last that starts at or before q
+  __device__ __forceinline__ int part_of(int q, int parts) const {
+    return (int)((((long long)q + 1) * parts - 1) / pieces);
   }
   __device__ __forceinline__ uint4 load(int q) const {
-    if (q > 0 && q < pieces - 1) return __ldg(reinterpret_cast<const uint4*>(base) + q);
-    return load_end(q);
+    if constexpr (HELD) {
+      return held[q - s0];
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(base) + q;
+      if (q == 0) p = held;                  // the ends, made up in shared memory
+      if (q == pieces - 1) p = held + 1;
+      return *p;
+    }
   }
-  // the first or last piece, which may reach outside the row
+  // the first or last piece, element by element
   __device__ __noinline__ uint4 load_end(int q) const {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     for (int j = 0; j < V; ++j) {
@@ -156,6 +207,20 @@ template <typename T> struct Pieces {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = to_f32(h[j]);
   }
+  // Largest value of a piece (NaNs apart: -inf or less than any other).
+  static __device__ __forceinline__ float max_of(const uint4& r) {
+    if constexpr (sizeof(T) == 4) {
+      float v[V];
+      values(r, v);
+      return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    } else {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                           __nv_bfloat162>::type;
+      const T2* h = reinterpret_cast<const T2*>(&r);
+      const T2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      return fmaxf(to_f32(m.x), to_f32(m.y));
+    }
+  }
   // This lane's pieces of the batch at b (32 * kShares consecutive pieces).
   __device__ __forceinline__ void batch(int b, int q1, uint4 (&r)[kShares]) const {
 #pragma unroll
@@ -164,23 +229,45 @@ template <typename T> struct Pieces {
       r[u] = q < q1 ? load(q) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  // f(values, index of the first) for this warp's pieces q0 .. q1, one a turn
-  template <typename F> __device__ __forceinline__ void each(int q0, int q1, F f) const {
+  // f(piece, its number) for this warp's pieces q0 .. q1, one a turn
+  template <typename F> __device__ __forceinline__ void each_piece(int q0, int q1, F f) const {
     int q = q0 + (int)(threadIdx.x & 31);
-    uint4 r0, r1, r2;
-    if (q < q1) r0 = load(q);
-    if (q + 32 < q1) r1 = load(q + 32);
-    if (q + 64 < q1) r2 = load(q + 64);
+    if constexpr (HELD) {
 #pragma unroll 1
-    for (; q < q1; q += 32) {
-      const uint4 r = r0;
-      r0 = r1;
-      r1 = r2;
-      if (q + 96 < q1) r2 = load(q + 96);
+      for (; q < q1; q += 32) f(load(q), q);
+    } else {
+      uint4 r0, r1, r2;               // the next three pieces in flight
+      if (q < q1) r0 = load(q);
+      if (q + 32 < q1) r1 = load(q + 32);
+      if (q + 64 < q1) r2 = load(q + 64);
+#pragma unroll 1
+      for (; q < q1; q += 32) {
+        const uint4 r = r0;
+        r0 = r1;
+        r1 = r2;
+        if (q + 96 < q1) r2 = load(q + 96);
+        f(r, q);
+      }
+    }
+  }
+  // f(values, index of the first) for them
+  template <typename F> __device__ __forceinline__ void each(int q0, int q1, F f) const {
+    each_piece(q0, q1, [&](const uint4& r, int q) {
       float v[V];
       values(r, v);
       f(v, q * V - mis);
-    }
+    });
+  }
+  // and for those whose largest value reaches `low`
+  template <typename F>
+  __device__ __forceinline__ void each_above(int q0, int q1, float low, F f) const {
+    each_piece(q0, q1, [&](const uint4& r, int q) {
+      if (max_of(r) >= low) {
+        float v[V];
+        values(r, v);
+        f(v, q * V - mis);
+      }
+    });
   }
 };
 
@@ -245,18 +332,18 @@ __device__ u64 block_scan(u64 v, Shared& sh, u64* total) {
   return before + inc - v;
 }
 
-// Sorts sh.list[0 .. size) descending; size a power of two, at least 2.
+// Sorts the joined list's first `size` keys descending; a power of two, at least 2.
 __device__ void sort_list(Shared& sh, int size) {
   __syncthreads();
   for (int len = 2; len <= size; len <<= 1) {
     for (int stride = len >> 1; stride > 0; stride >>= 1) {
       for (int i = threadIdx.x; i < size / 2; i += kThreads) {
         const int p = 2 * i - (i & (stride - 1));
-        const u64 a = sh.list[p], b = sh.list[p + stride];
+        const u64 a = keys(sh)[p], b = keys(sh)[p + stride];
         const bool up = (p & len) != 0;              // ascending stretch
         if (up ? a > b : a < b) {
-          sh.list[p] = b;
-          sh.list[p + stride] = a;
+          keys(sh)[p] = b;
+          keys(sh)[p + stride] = a;
         }
       }
       // a warp's pairs of strides <= 32 stay within its own 64 entries
@@ -275,28 +362,39 @@ __device__ __forceinline__ int pow2_at_least(int v) {
   return p;
 }
 
-__device__ __forceinline__ void append(Shared& sh, u64 key) {
+// A block's own list; a block alone fills the joined one.
+__device__ __forceinline__ u64* own_list(Shared& sh, const Team& team) {
+  return team.size > 1 ? sh.list : keys(sh);
+}
+__device__ __forceinline__ void append(Shared& sh, const Team& team, u64 key) {
   const uint32_t at = atomicAdd(&sh.listed, 1u);
-  if (at < (uint32_t)kList) sh.list[at] = key;
+  if (at < (uint32_t)(team.size > 1 ? kLocal : kList)) own_list(sh, team)[at] = key;
 }
 
-// Tokens listed by all blocks of the cluster.  After a sync that follows the
-// gathering; the caller syncs before the lists are used again.
+// Tokens listed by all blocks of the cluster; more than kList when they do not
+// fit.  After a sync that follows the gathering; the caller syncs before the
+// lists are used again.
 __device__ __forceinline__ u64 listed_by_all(Shared& sh, const Team& team) {
+  if (team.size == 1) return sh.listed;
   u64 total = 0;
-  team.over(&sh.listed, [&](uint32_t c, int) { total += c; });
+  team.over(&sh.listed, [&](uint32_t c, int) {
+    total += c <= (uint32_t)kLocal ? (u64)c : (u64)kList + 1ull;
+  });
   return total;
 }
 
-// The first block's list gets those of the others appended (they fit).
+// The first block's joined list gets all blocks' lists (they fit).
 __device__ void join_lists(Shared& sh, const Team& team) {
-  if (team.rank != 0) return;
-  uint32_t at = sh.listed;
-  for (int r = 1; r < team.size; ++r) {
-    const uint32_t c = *team.of(&sh.listed, r);
-    const u64* src = team.of(&sh.list[0], r);
-    for (uint32_t i = threadIdx.x; i < c; i += kThreads) sh.list[at + i] = src[i];
-    at += c;
+  if (team.rank != 0 || team.size == 1) return;
+  const int warp = threadIdx.x >> 5;                   // one warp a block's list
+  if (warp < team.size) {
+    uint32_t at = 0, mine = 0;
+    team.over(&sh.listed, [&](uint32_t c, int k) {
+      if (k < warp) at += c;
+      if (k == warp) mine = c;
+    });
+    const u64* src = team.of(&sh.list[0], warp);
+    for (uint32_t i = threadIdx.x & 31; i < mine; i += 32) keys(sh)[at + i] = src[i];
   }
   __syncthreads();
 }
@@ -321,7 +419,7 @@ __device__ __forceinline__ void write_draw(const SampleArgs& a, int row, int id,
 }
 
 // Top-k, top-p, min-p and draw among the `len` tokens of the first block's
-// list, which hold the first top_k by rank (or, fewer, all with a weight).
+// joined list, which hold the first top_k by rank (or, fewer, all with a weight).
 // Short lists: every token counts the tokens and sums the weights before it,
 // by rank and then, among the kept, by index.
 __device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Shared& sh,
@@ -333,15 +431,15 @@ __device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Sh
   float e = 0.f;
   uint32_t w = 0;
   if (p < len) {
-    key = sh.list[p];
+    key = keys(sh)[p];
     e = Row::e(r.depth(rank_logit(key)));
     w = Row::weight(e);
-    if (part == 0) sh.weight[p] = w;
+    if (part == 0) weights(sh)[p] = w;
   }
   __syncthreads();
   u64 before = 0;                      // weights before it by rank, and how many tokens
   for (int j = part; j < len; j += 4)
-    if (sh.list[j] > key) before += ((u64)sh.weight[j] << 8) | 1u;
+    if (keys(sh)[j] > key) before += ((u64)weights(sh)[j] << 8) | 1u;
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
   const bool in_k = p < len && (int)(before & 255u) < top_k;
@@ -351,12 +449,12 @@ __device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Sh
   const bool keep = in_k && (top_p >= 1.f || before < nucleus_target(top_p, sum)) && e >= r.min_p;
   u64 kept;
   block_scan(keep && part == 0 ? w : 0u, sh, &kept);
-  if (p < len && !keep && part == 0) sh.weight[p] = 0u;
+  if (p < len && !keep && part == 0) weights(sh)[p] = 0u;
   __syncthreads();
   u64 run = 0;                         // kept weights of lower indices
   const uint32_t idx = rank_index(key);
   for (int j = part; j < len; j += 4)
-    if (rank_index(sh.list[j]) < idx) run += sh.weight[j];
+    if (rank_index(keys(sh)[j]) < idx) run += weights(sh)[j];
   run += __shfl_xor_sync(0xFFFFFFFFu, run, 1);
   run += __shfl_xor_sync(0xFFFFFFFFu, run, 2);
   const u64 target = draw_target(u, kept);
@@ -368,7 +466,7 @@ __device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Sh
 __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Shared& sh, const Row& r, int len,
                                   int top_k, float top_p, float u) {
   const int size = pow2_at_least(len);
-  for (int i = len + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0ull;
+  for (int i = len + threadIdx.x; i < size; i += kThreads) keys(sh)[i] = 0ull;
   sort_list(sh, size);
   constexpr int kPer = kList / kThreads;
   const int per = (size + kThreads - 1) / kThreads;    // 1..kPer consecutive entries a thread
@@ -382,7 +480,7 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
     w[i] = 0u;
     e[i] = 0.f;
     if (i < per && p < limit) {
-      e[i] = Row::e(r.depth(rank_logit(sh.list[p])));
+      e[i] = Row::e(r.depth(rank_logit(keys(sh)[p])));
       w[i] = Row::weight(e[i]);
       mine += w[i];
     }
@@ -398,7 +496,7 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
     if (i < per && p < limit && before < reach && e[i] >= r.min_p)
       kept += ((u64)w[i] << 12) | 1u;                  // up to 2^11 weights of 2^31, and a count
     before += w[i];
-    if (i < per && p < kList) sh.weight[p] = w[i];
+    if (i < per && p < kList) weights(sh)[p] = w[i];
   }
   u64 kept_total;
   block_scan(kept, sh, &kept_total);
@@ -410,13 +508,13 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x + i * kThreads;
-    by_index[i] = p < keep ? ((sh.list[p] & kIndexMask) << 32) | (u64)p : 0ull;
+    by_index[i] = p < keep ? ((keys(sh)[p] & kIndexMask) << 32) | (u64)p : 0ull;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x + i * kThreads;
-    if (p < size2) sh.list[p] = by_index[i];
+    if (p < size2) keys(sh)[p] = by_index[i];
   }
   sort_list(sh, size2);
   const int per2 = (size2 + kThreads - 1) / kThreads;
@@ -424,7 +522,7 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x * per2 + i;
-    w[i] = (i < per2 && p < keep) ? sh.weight[(uint32_t)sh.list[p]] : 0u;
+    w[i] = (i < per2 && p < keep) ? weights(sh)[(uint32_t)keys(sh)[p]] : 0u;
     mine += w[i];
   }
   before = block_scan(mine, sh, &sum);
@@ -432,135 +530,152 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (before <= target && target < before + w[i])
-      write_draw(a, row, (int)(~(uint32_t)(sh.list[threadIdx.x * per2 + i] >> 32) & kIndexMask),
+      write_draw(a, row, (int)(~(uint32_t)(keys(sh)[threadIdx.x * per2 + i] >> 32) & kIndexMask),
                  w[i], kept_sum);
     before += w[i];
   }
 }
 
-// The rank key of the last token of the shortest prefix, in rank order among
-// the tokens with a weight and a rank key of at least `from`, whose count
-// (COUNT) or sum of weights reaches a target; 0 when there is none.  For a
-// nucleus the target follows from the first histogram, whose total is the sum
-// of all weights.  *mass_out gets the prefix's sum of weights.
-template <bool COUNT, typename T>
-__device__ __noinline__ u64 find_cut(const Pieces<T>& pc, int q0, int q1, Shared& sh, const Team& team,
-                        const Row& r, int top_k, float top_p, u64 from, u64* mass_out) {
-  constexpr int V = Pieces<T>::V;
-  constexpr int kDigitBits = 7;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 before_count = 0, before_mass = 0, target = (u64)top_k;
-  float lowest = from ? rank_logit(from) : __int_as_float(0xFF800000);   // of the open tokens
-  int bin = -1;                      // chosen quarter octave
-  u64 prefix = 0;                    // chosen leading digits of the rank key
-  int shift = 8 * kDigitBits;        // bits of the rank key (32 + 20) still open
-  for (;;) {
-    const bool first = bin < 0;
-    const int dshift = first ? shift : shift - kDigitBits;
-    if (threadIdx.x == 0) sh.digit = -1;
-    __syncthreads();
-    auto add = [&](int d, uint32_t w) {
-      if (w != 0u) atomicAdd(&sh.low[d][lane], w & 0xFFFFu);
-      if (w > 0xFFFFu) atomicAdd(&sh.high[d][lane], w >> 16);
-      if (COUNT && w != 0u) atomicAdd(&sh.count[d][lane], 1u);
-    };
-    if (first && from == 0ull) {
-      pc.each(q0, q1, [&](const float (&v)[V], int) {
+__device__ __forceinline__ void clear_hist(Shared& sh) {
+  uint32_t* h = &sh.hist.low[0][0];      // low, high, count
+  for (int i = threadIdx.x; i < 3 * kBins * kCopies; i += kThreads) h[i] = 0u;
+}
+
+// Folds the copies of the histograms into bin_mass and bin_count.
+template <bool COUNT, bool MASS> __device__ __forceinline__ void fold_hist(Shared& sh) {
+  const int copy = threadIdx.x & (kCopies - 1);
+  for (int d = threadIdx.x / kCopies; d < kBins; d += kThreads / kCopies) {
+    u64 m = MASS ? (u64)sh.hist.low[d][copy] + ((u64)sh.hist.high[d][copy] << 16) : 0ull;
+    uint32_t c = COUNT ? sh.hist.count[d][copy] : 0u;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float x = r.depth(v[j]);
-          add(Row::bin(x), Row::weight(Row::e(x)));
-        }
-      });
-    } else {
-      pc.each(q0, q1, [&](const float (&v)[V], int i0) {
-#pragma unroll 1
-        for (int j = 0; j < V; ++j) {
-          const float l = v[j];
-          if (!(l >= lowest)) continue;
-          const float x = r.depth(l);
-          const u64 key = rank_key(l, (uint32_t)(i0 + j));
-          if (key < from) continue;
-          int d = Row::bin(x);
-          if (!first) {
-            if (d != bin || (key >> shift) != prefix) continue;
-            d = kBins - 1 - (int)((key >> dshift) & (kBins - 1));
-          }
-          add(d, Row::weight(Row::e(x)));
-        }
-      });
+    for (int x = kCopies / 2; x > 0; x >>= 1) {
+      if (MASS) m += __shfl_xor_sync(0xFFFFFFFFu, m, x);
+      if (COUNT) c += __shfl_xor_sync(0xFFFFFFFFu, c, x);
     }
-    __syncthreads();
-    // fold the lanes' copies, and clear them for the next time
-    for (int d = warp; d < kBins; d += kWarps) {
-      const u64 m = warp_sum((u64)sh.low[d][lane] + ((u64)sh.high[d][lane] << 16));
-      sh.low[d][lane] = 0u;
-      sh.high[d][lane] = 0u;
-      uint32_t c = 0;
-      if (COUNT) {
-        c = __reduce_add_sync(0xFFFFFFFFu, sh.count[d][lane]);
-        sh.count[d][lane] = 0u;
+    if (copy == 0) {
+      if (MASS) sh.bin_mass[d] = m;
+      if (COUNT) sh.bin_count[d] = c;
+    }
+  }
+}
+
+// Where a row's cut is being looked for.
+struct Search {
+  u64 target;          // count or weight that the prefix has to reach
+  u64 from;            // rank key of the last candidate (0: all)
+  u64 before_count = 0, before_mass = 0;     // ahead of the open tokens
+  int bin = -1;        // chosen quarter octave
+  u64 prefix = 0;      // chosen leading digits of the rank key
+  int shift = 8 * 7;   // bits of the rank key (32 + 20) still open
+};
+
+// One round: a histogram of the open tokens, by quarter octave first and then
+// by the next seven bits of the rank key, and in it the digit at which the
+// running count (COUNT) or weight reaches the target.  For a nucleus the
+// target follows from the first histogram, whose total is the sum of all
+// weights.  False when the total stays below the target; *total_mass gets it.
+template <bool COUNT, typename P>
+__device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& sh,
+                                          const Team& team, const Row& r, float top_p, Search& f,
+                                          u64* total_mass) {
+  constexpr int V = P::V;
+  constexpr int kDigitBits = 7;
+  const int copy = threadIdx.x & (kCopies - 1);
+  const bool first = f.bin < 0;
+  const int dshift = first ? f.shift : f.shift - kDigitBits;
+  clear_hist(sh);
+  if (threadIdx.x == 0) {
+    sh.digit = -1;
+    sh.listed = 0u;
+  }
+  __syncthreads();
+  constexpr int kHigh = kBins * kCopies, kCount = 2 * kHigh;     // from a low sum to the others
+  uint32_t* const hist = &sh.hist.low[0][copy];
+  if (first && f.from == 0ull) {
+    pc.each(q0, q1, [&](const float (&v)[V], int) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float x = r.depth(v[j]);
+        uint32_t high, low;
+        Row::halves(Row::e(x), &high, &low);
+        uint32_t* h = hist + Row::bin_if_weight(x) * kCopies;
+        if (x > -31.5f) atomicAdd(h, low - Row::kOne);
+        if (high != Row::kOne) atomicAdd(h + kHigh, high - Row::kOne);
+        if (COUNT && (high | low) != Row::kOne) atomicAdd(h + kCount, 1u);
       }
-      if (lane == 0) {
-        sh.bin_mass[d] = m;
-        sh.bin_count[d] = c;
-      }
-    }
-    team.sync();
-    // every block joins the histograms and comes to the same choice
-    u64 cnt = 0, mass = 0;
-    if (threadIdx.x < kBins) {
-      team.over(&sh.bin_mass[threadIdx.x], [&](u64 m, int) { mass += m; });
-      if (COUNT) team.over(&sh.bin_count[threadIdx.x], [&](uint32_t c, int) { cnt += c; });
-    }
-    u64 total_mass, total_count;
-    const u64 to_mass = before_mass + block_scan(mass, sh, &total_mass);
-    const u64 to_count = COUNT ? before_count + block_scan(cnt, sh, &total_count) : 0ull;
-    if (!COUNT && first) target = nucleus_target(top_p, total_mass);
-    const u64 lo = COUNT ? to_count : to_mass, hi = lo + (COUNT ? cnt : mass);
-    if (lo < target && target <= hi) {
-      sh.digit = (int)threadIdx.x;
-      sh.before_count = to_count;
-      sh.before_mass = to_mass;
-    }
-    if (threadIdx.x == 0) sh.listed = 0u;
-    __syncthreads();
-    const int digit = sh.digit;
-    if (digit < 0) {                 // (top-k only: fewer tokens than that have a weight)
-      *mass_out = total_mass;
-      team.sync();
-      return 0ull;
-    }
-    before_count = sh.before_count;
-    before_mass = sh.before_mass;
-    if (first) {
-      bin = digit;
-    } else {
-      prefix = (prefix << kDigitBits) | (u64)(kBins - 1 - digit);
-      shift = dshift;
-    }
-    // gather the open tokens; the bounds are generous, the test is exact
-    const float low_b = r.top - ((float)bin + 0.75f) / (4.f * r.c);
-    const float high_b = r.top - ((float)bin - 0.75f) / (4.f * r.c);
-    if (low_b > lowest) lowest = low_b;
+    });
+  } else {
+    const float lowest = f.from ? rank_logit(f.from) : __int_as_float(0xFF800000);
     pc.each(q0, q1, [&](const float (&v)[V], int i0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (v[j] >= lowest && v[j] <= high_b) {
-          const float x = r.depth(v[j]);
-          const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
-          if (Row::weight(Row::e(x)) != 0u && Row::bin(x) == bin && key >= from &&
-              (key >> shift) == prefix)
-            append(sh, key);
+      for (int j = 0; j < V; ++j) {
+        const float l = v[j];
+        if (!(l >= lowest)) continue;
+        const float x = r.depth(l);
+        const u64 key = rank_key(l, (uint32_t)(i0 + j));
+        if (key < f.from) continue;
+        int d = Row::bin(x);
+        if (!first) {
+          if (d != f.bin || (key >> f.shift) != f.prefix) continue;
+          d = kBins - 1 - (int)((key >> dshift) & (kBins - 1));
         }
+        const uint32_t w = Row::weight(Row::e(x));
+        if (w == 0u) continue;
+        atomicAdd(hist + d * kCopies, w & 0xFFFFu);
+        atomicAdd(hist + d * kCopies + kHigh, w >> 16);
+        if (COUNT) atomicAdd(hist + d * kCopies + kCount, 1u);
+      }
     });
-    team.sync();
-    const u64 open = listed_by_all(sh, team);
-    if (open <= (u64)kList) break;
-    team.sync();                     // counted by all before the next round clears
   }
-  // the first block ranks the open tokens and finds the cut
-  const int len = (int)listed_by_all(sh, team);
+  __syncthreads();
+  fold_hist<COUNT, true>(sh);
+  team.sync();
+  // every block joins the histograms and comes to the same choice
+  u64 cnt = 0, mass = 0;
+  if (threadIdx.x < kBins) {
+    team.over(&sh.bin_mass[threadIdx.x], [&](u64 m, int) { mass += m; });
+    if (COUNT) team.over(&sh.bin_count[threadIdx.x], [&](uint32_t c, int) { cnt += c; });
+  }
+  u64 total, total_count;
+  const u64 to_mass = f.before_mass + block_scan(mass, sh, &total);
+  const u64 to_count = COUNT ? f.before_count + block_scan(cnt, sh, &total_count) : 0ull;
+  *total_mass = total;
+  if (!COUNT && first) f.target = nucleus_target(top_p, total);
+  const u64 lo = COUNT ? to_count : to_mass, hi = lo + (COUNT ? cnt : mass);
+  if (lo < f.target && f.target <= hi) {
+    sh.digit = (int)threadIdx.x;
+    sh.before_count = to_count;
+    sh.before_mass = to_mass;
+  }
+  __syncthreads();
+  const int digit = sh.digit;
+  if (digit < 0) return false;
+  f.before_count = sh.before_count;
+  f.before_mass = sh.before_mass;
+  if (first) {
+    f.bin = digit;
+  } else {
+    f.prefix = (f.prefix << kDigitBits) | (u64)(kBins - 1 - digit);
+    f.shift = dshift;
+  }
+  return true;
+}
+
+// Generous bounds of the logits of quarter octave `bin`: no token of it lies
+// outside, and none of a lower or higher one beyond the next.
+__device__ __forceinline__ float bin_low(const Row& r, int bin) {
+  return r.top - ((float)bin + 0.75f) / (4.f * r.c);
+}
+__device__ __forceinline__ float bin_high(const Row& r, int bin) {
+  return r.top - ((float)bin - 0.75f) / (4.f * r.c);
+}
+
+// The open tokens, joined and ranked by the first block: the rank key of the
+// one at which the target is reached, and (*mass) the weights up to it.
+// Ends with a sync.
+template <bool COUNT>
+__device__ __noinline__ u64 rank_open(Shared& sh, const Team& team, const Row& r, const Search& f,
+                                      int len, u64* mass_out) {
   join_lists(sh, team);
   if (team.rank == 0) {
     if (len <= kCountRank) {
@@ -568,51 +683,46 @@ __device__ __noinline__ u64 find_cut(const Pieces<T>& pc, int q0, int q1, Shared
       u64 key = 0;
       uint32_t w = 0;
       if (p < len) {
-        key = sh.list[p];
+        key = keys(sh)[p];
         w = Row::weight(Row::e(r.depth(rank_logit(key))));
-        if (part == 0) sh.weight[p] = w;
+        if (part == 0) weights(sh)[p] = w;
       }
       __syncthreads();
       u64 ahead = 0;
       for (int j = part; j < len; j += 4)
-        if (sh.list[j] > key) ahead += ((u64)sh.weight[j] << 8) | 1u;
+        if (keys(sh)[j] > key) ahead += ((u64)weights(sh)[j] << 8) | 1u;
       ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, 1);
       ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, 2);
-      const u64 mass = before_mass + (ahead >> 8);
-      const u64 lo = COUNT ? before_count + (ahead & 255u) : mass;
+      const u64 mass = f.before_mass + (ahead >> 8);
+      const u64 lo = COUNT ? f.before_count + (ahead & 255u) : mass;
       const u64 hi = lo + (COUNT ? 1ull : (u64)w);
-      if (p < len && part == 0 && lo < target && target <= hi) {
+      if (p < len && part == 0 && lo < f.target && f.target <= hi) {
         sh.cut = key;
         sh.sum = mass + w;
       }
     } else {
       const int size = pow2_at_least(len);
-      for (int i = len + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0ull;
+      for (int i = len + threadIdx.x; i < size; i += kThreads) keys(sh)[i] = 0ull;
       sort_list(sh, size);
-      constexpr int kPer = kList / kThreads;
-      const int per = (size + kThreads - 1) / kThreads;
-      uint32_t w[kPer];
+      const int per = (size + kThreads - 1) / kThreads;    // consecutive entries a thread
+      const int p0 = threadIdx.x * per, p1 = min(p0 + per, len);
       u64 mine = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int p = threadIdx.x * per + i;
-        w[i] = (i < per && p < len) ? Row::weight(Row::e(r.depth(rank_logit(sh.list[p])))) : 0u;
-        mine += w[i];
+      for (int p = p0; p < p1; ++p) {
+        const uint32_t w = Row::weight(Row::e(r.depth(rank_logit(keys(sh)[p]))));
+        weights(sh)[p] = w;
+        mine += w;
       }
       u64 total;
-      u64 mass = before_mass + block_scan(mine, sh, &total);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int p = threadIdx.x * per + i;
-        if (i < per && p < len) {
-          const u64 lo = COUNT ? before_count + (u64)p : mass;
-          const u64 hi = lo + (COUNT ? 1ull : (u64)w[i]);
-          if (lo < target && target <= hi) {
-            sh.cut = sh.list[p];
-            sh.sum = mass + w[i];
-          }
+      u64 mass = f.before_mass + block_scan(mine, sh, &total);
+      for (int p = p0; p < p1; ++p) {
+        const uint32_t w = weights(sh)[p];
+        const u64 lo = COUNT ? f.before_count + (u64)p : mass;
+        const u64 hi = lo + (COUNT ? 1ull : (u64)w);
+        if (lo < f.target && f.target <= hi) {
+          sh.cut = keys(sh)[p];
+          sh.sum = mass + w;
         }
-        mass += w[i];
+        mass += w;
       }
     }
   }
@@ -623,39 +733,54 @@ __device__ __noinline__ u64 find_cut(const Pieces<T>& pc, int q0, int q1, Shared
   return cut;
 }
 
-// The draw over the whole row, by index, among tokens with e >= min_p and
-// (CUT) a rank key of at least `cut`.
-template <bool CUT, typename T>
-__device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const Pieces<T>& pc, int q0, int q1,
-                            Shared& sh, const Team& team, const Row& r, u64 cut, float u) {
-  constexpr int V = Pieces<T>::V;
+// The rank key of the last token of the shortest prefix that reaches the
+// search's target; 0 when all tokens together do not.  *mass_out gets the
+// prefix's sum of weights.  `f` may have its first round behind it (`started`).
+template <bool COUNT, typename P>
+__device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, Shared& sh, const Team& team,
+                                     const Row& r, float top_p, Search& f, bool started,
+                                     u64* mass_out) {
+  constexpr int V = P::V;
+  for (;;) {
+    if (!started && !search_round<COUNT>(pc, q0, q1, sh, team, r, top_p, f, mass_out)) {
+      team.sync();
+      return 0ull;
+    }
+    if (!started) {
+      // gather the open tokens; the bounds are generous, the test is exact
+      const float low = bin_low(r, f.bin), high = bin_high(r, f.bin);
+      pc.each_above(q0, q1, low, [&](const float (&v)[V], int i0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (v[j] >= low && v[j] <= high) {
+            const float x = r.depth(v[j]);
+            const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
+            if (Row::weight(Row::e(x)) != 0u && Row::bin(x) == f.bin && key >= f.from &&
+                (key >> f.shift) == f.prefix)
+              append(sh, team, key);
+          }
+      });
+      team.sync();
+      const u64 open = listed_by_all(sh, team);
+      if (open <= (u64)kList) return rank_open<COUNT>(sh, team, r, f, (int)open, mass_out);
+    }
+    started = false;
+    team.sync();                       // counted by all before the next round clears
+  }
+}
+
+// The draw, once every warp's stretches have their sums in sh.seg: `per`
+// batches each; among tokens with e >= min_p and (CUT) a rank key >= `cut`.
+template <bool CUT, typename P>
+__device__ __noinline__ void draw_by_stretch(const SampleArgs& a, int row, const P& pc, int q0,
+                                             int q1, int per, Shared& sh, const Team& team,
+                                             const Row& r, u64 cut, float u) {
+  constexpr int V = P::V;
   constexpr int kBatch = 32 * kShares;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float lowest = rank_logit(cut);
-  auto kept = [&](float l, int idx) -> uint32_t {
-    const float e = Row::e(r.depth(l));
-    const uint32_t w = Row::weight(e);
-    if constexpr (CUT) {
-      if (l == lowest && rank_key(l, (uint32_t)idx) < cut) return 0u;
-    }
-    return e >= r.min_p ? w : 0u;
-  };
-  const int per = ((q1 - q0 + kBatch - 1) / kBatch + kSegs - 1) / kSegs;   // batches a stretch
-  u64 warp_total = 0;
-  int seg = 0;
-  for (int b0 = q0; b0 < q1; b0 += per * kBatch, ++seg) {
-    const int b1 = min(q1, b0 + per * kBatch);
-    u64 mine = 0;
-    pc.each(b0, b1, [&](const float (&v)[V], int i0) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (!CUT || v[j] >= lowest) mine += kept(v[j], i0 + j);
-    });
-    mine = warp_sum(mine);
-    if (lane == 0) sh.seg[warp][seg] = mine;
-    warp_total += mine;
-  }
-  __syncthreads();
+  const int segs = per > 0 ? (q1 - q0 + per * kBatch - 1) / (per * kBatch) : 0;
+  const u64 warp_total = warp_sum(lane < segs ? sh.seg[warp][lane] : 0ull);
   if (lane == 0) sh.red[warp] = warp_total;
   __syncthreads();
   u64 before = 0, block_total = 0;
@@ -671,56 +796,179 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const Pie
     sum += t;
   });
   const u64 target = draw_target(u, sum);
-  if (before <= target && target < before + warp_total) {
-    // this warp's part holds the draw: find the stretch, then walk it
-    seg = 0;
-    while (target >= before + sh.seg[warp][seg]) before += sh.seg[warp][seg++];
-    const int e0 = q0 + seg * per * kBatch, e1 = min(q1, e0 + per * kBatch);
-    bool found = false;
-    for (int b = e0; b < e1 && !found; b += kBatch) {
-      uint4 raw[kShares];
-      pc.batch(b, e1, raw);
+  if (!(before <= target && target < before + warp_total)) return;
+  // this warp's part holds the draw: find the stretch, then walk it
+  int seg = 0;
+  while (target >= before + sh.seg[warp][seg]) before += sh.seg[warp][seg++];
+  const int e0 = q0 + seg * per * kBatch, e1 = min(q1, e0 + per * kBatch);
+  for (int b = e0; b < e1; b += kBatch) {
+    uint4 raw[kShares];
+    pc.batch(b, e1, raw);
 #pragma unroll 1
-      for (int s = 0; s < kShares; ++s) {
-        const int q = b + s * 32 + lane;
-        const uint4 piece = raw[0];
+    for (int s = 0; s < kShares; ++s) {
+      const int q = b + s * 32 + lane;
+      const uint4 piece = raw[0];
 #pragma unroll
-        for (int i = 1; i < kShares; ++i) raw[i - 1] = raw[i];
-        uint32_t w[V];
-        u64 mine = 0;
-        float v[V];
-        Pieces<T>::values(piece, v);
+      for (int i = 1; i < kShares; ++i) raw[i - 1] = raw[i];
+      uint32_t w[V];
+      u64 mine = 0;
+      float v[V];
+      P::values(piece, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float e = Row::e(r.depth(v[j]));
+        bool kept = q < e1 && e >= r.min_p;
+        if (CUT) kept = kept && v[j] >= lowest && rank_key(v[j], (uint32_t)(q * V - pc.mis + j)) >= cut;
+        w[j] = kept ? Row::weight(e) : 0u;
+        mine += w[j];
+      }
+      const u64 inc = warp_scan(mine);
+      const u64 step = __shfl_sync(0xFFFFFFFFu, inc, 31);
+      if (target < before + step) {
+        u64 at = before + inc - mine;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          w[j] = q < e1 && (!CUT || v[j] >= lowest) ? kept(v[j], q * V - pc.mis + j) : 0u;
-          mine += w[j];
+          if (at <= target && target < at + w[j])
+            write_draw(a, row, q * V - pc.mis + j, w[j], sum);
+          at += w[j];
         }
-        const u64 inc = warp_scan(mine);
-        const u64 step = __shfl_sync(0xFFFFFFFFu, inc, 31);
-        if (!found && target < before + step) {
-          u64 at = before + inc - mine;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            if (at <= target && target < at + w[j])
-              write_draw(a, row, q * V - pc.mis + j, w[j], sum);
-            at += w[j];
-          }
-          found = true;
-        }
-        before += step;
+        return;
       }
+      before += step;
     }
   }
 }
 
+__device__ __forceinline__ int batches_per_stretch(int q0, int q1) {
+  constexpr int kBatch = 32 * kShares;
+  return ((q1 - q0 + kBatch - 1) / kBatch + kSegs - 1) / kSegs;
+}
+
+// f(first piece, one past the last) -> this lane's sum, for every stretch of
+// this warp; the warp's sums go to sh.seg.
+template <typename F>
+__device__ __forceinline__ void sum_stretches(int q0, int q1, int per, Shared& sh, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int step = per * 32 * kShares;
+  int seg = 0;
+  for (int b = q0; b < q1; b += step, ++seg) {
+    const u64 s = warp_sum(f(b, min(q1, b + step)));
+    if (lane == 0) sh.seg[warp][seg] = s;
+  }
+}
+
+// The draw over the whole row among tokens with e >= min_p (0 without MIN_P)
+// and (CUT) a rank key of at least `cut`.
+template <bool CUT, bool MIN_P, typename P>
+__device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& pc, int q0, int q1,
+                                         Shared& sh, const Team& team, const Row& r, u64 cut,
+                                         float u) {
+  constexpr int V = P::V;
+  const float lowest = rank_logit(cut);
+  const int per = batches_per_stretch(q0, q1);
+  sum_stretches(q0, q1, per, sh, [&](int b0, int b1) {
+    u64 mine = 0;
+    if constexpr (CUT) {
+      pc.each_above(b0, b1, lowest, [&](const float (&v)[V], int i0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (!(v[j] >= lowest) ||
+              (v[j] == lowest && rank_key(v[j], (uint32_t)(i0 + j)) < cut))
+            continue;
+          const float e = Row::e(r.depth(v[j]));
+          mine += e >= r.min_p ? Row::weight(e) : 0u;
+        }
+      });
+    } else {
+      // sums of the halves, kOne and all, modulo 2^32: a stretch has fewer than
+      // 2^16 tokens of a lane, so the halves' own sums stay below it
+      uint32_t high = 0, low = 0, pieces = 0;
+      pc.each(b0, b1, [&](const float (&v)[V], int) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          float e = Row::e(r.depth(v[j]));
+          if (MIN_P) e = e >= r.min_p ? e : 0.f;
+          uint32_t h, l;
+          Row::halves(e, &h, &l);
+          high += h;
+          low += l;
+        }
+        ++pieces;
+      });
+      const uint32_t ones = pieces * (uint32_t)V * Row::kOne;
+      mine = ((u64)(high - ones) << 16) + (u64)(low - ones);
+    }
+    return mine;
+  });
+  __syncthreads();
+  draw_by_stretch<CUT>(a, row, pc, q0, q1, per, sh, team, r, cut, u);
+}
+
+// A nucleus (within the tokens of rank key >= from) and the draw in it.
+template <typename P>
+__device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P& pc, int q0,
+                                          int q1, Shared& sh, const Team& team, const Row& r,
+                                          u64 from, float top_p, float u) {
+  constexpr int V = P::V;
+  Search f;
+  f.from = from;
+  u64 mass;
+  // (always found: the largest weight is 2^31)
+  search_round<false>(pc, q0, q1, sh, team, r, top_p, f, &mass);
+  const float low = bin_low(r, f.bin);
+  const int per = batches_per_stretch(q0, q1);
+  sum_stretches(q0, q1, per, sh, [&](int b0, int b1) {
+    u64 mine = 0;
+    pc.each_above(b0, b1, low, [&](const float (&v)[V], int i0) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (!(v[j] >= low)) continue;
+        const float x = r.depth(v[j]);
+        const float e = Row::e(x);
+        const uint32_t w = Row::weight(e);
+        const int b = Row::bin(x);
+        if (b < f.bin) {
+          mine += e >= r.min_p ? w : 0u;           // above the open ones: kept
+        } else if (b == f.bin && w != 0u) {
+          const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
+          if (key >= from) append(sh, team, key);
+        }
+      }
+    });
+    return mine;
+  });
+  team.sync();
+  const u64 open = listed_by_all(sh, team);
+  if (open > (u64)kList) {
+    const u64 cut = find_cut<false>(pc, q0, q1, sh, team, r, top_p, f, true, &mass);
+    draw_in_row<true, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    return;
+  }
+  const u64 cut = rank_open<false>(sh, team, r, f, (int)open, &mass);
+  // this block's open tokens that are kept join their stretches' sums
+  const int parts = team.size * kWarps;
+  for (int i = threadIdx.x; i < (int)sh.listed; i += kThreads) {
+    const u64 key = own_list(sh, team)[i];
+    const float e = Row::e(r.depth(rank_logit(key)));
+    if (key < cut || !(e >= r.min_p)) continue;
+    const int q = ((int)rank_index(key) + pc.mis) / V;
+    const int part = pc.part_of(q, parts);
+    const int p0 = pc.first(part, parts), p1 = pc.first(part + 1, parts);
+    const int seg = (q - p0) / (batches_per_stretch(p0, p1) * 32 * kShares);
+    atomicAdd(&sh.seg[part - team.rank * kWarps][seg], (u64)Row::weight(e));
+  }
+  __syncthreads();
+  draw_by_stretch<true>(a, row, pc, q0, q1, per, sh, team, r, cut, u);
+}
+
 // A row whose maximum is +inf: the infinite logits share the draw, a weight
 // of 2^31 each, ranked by index.
-template <typename T>
-__device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const Pieces<T>& pc,
+template <typename P>
+__device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P& pc,
                                            int q0, int q1, Shared& sh, const Team& team, int top_k,
                                            float top_p, float u) {
-  constexpr int V = Pieces<T>::V;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int V = P::V;
+  const int lane = threadIdx.x & 31;
   const float inf = __int_as_float(0x7F800000);
   u64 mine = 0;
   pc.each(q0, q1, [&](const float (&v)[V], int) {
@@ -744,7 +992,7 @@ __device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P
   for (int q = q0 + lane; q - lane < q1; q += 32) {
     float v[V];
     int c = 0;
-    if (q < q1) Pieces<T>::values(pc.load(q), v);
+    if (q < q1) P::values(pc.load(q), v);
 #pragma unroll
     for (int j = 0; j < V; ++j) c += q < q1 && v[j] == inf;
     const u64 inc = warp_scan((u64)c);
@@ -757,26 +1005,54 @@ __device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P
   }
 }
 
-template <typename T>
+template <typename T, bool HELD>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  constexpr int V = Pieces<T>::V;
+  using P = Pieces<T, HELD>;
+  constexpr int V = P::V;
   const Team team;
   const int row = blockIdx.x / team.size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < kBins * 32; i += kThreads) {
-    (&sh.low[0][0])[i] = 0u;
-    (&sh.high[0][0])[i] = 0u;
-    (&sh.count[0][0])[i] = 0u;
+  P pc(reinterpret_cast<const T*>(a.logits) + (size_t)row * a.n, a.n, smem + sizeof(Shared));
+  // this warp's pieces
+  const int parts = team.size * kWarps, part = team.rank * kWarps + warp;
+  const int q0 = pc.first(part, parts), q1 = pc.first(part + 1, parts);
+  pc.s0 = pc.first(team.rank * kWarps, parts);
+  if (threadIdx.x == 0) {
+    for (int c = 0; c < kChunks; ++c) mbar_init(&sh.bars[c], 1);
+    sh.failed = 0;
+    sh.listed = 0u;
+    sh.digit = -1;
+    sh.cut = 0ull;
+    sh.sum = 0ull;
+    fence_barrier_init();
   }
+  clear_hist(sh);
+  __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
-  const Pieces<T> pc(reinterpret_cast<const T*>(a.logits) + (size_t)row * a.n, a.n);
-  // this warp's pieces
-  const int part = team.rank * kWarps + warp, parts = team.size * kWarps;
-  const int q0 = (int)((long long)pc.pieces * part / parts);
-  const int q1 = (int)((long long)pc.pieces * (part + 1) / parts);
+
+  if constexpr (HELD) {
+    if (threadIdx.x == 0) {
+      // whole pieces inside the row; the ends are read one element at a time
+      for (int c = 0; c < kChunks; ++c) {
+        const int w0 = team.rank * kWarps + c * (kWarps / kChunks);
+        const int b0 = max(pc.first(w0, parts), 1);
+        const int b1 = min(pc.first(w0 + kWarps / kChunks, parts), pc.pieces - 1);
+        const uint32_t bytes = b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
+        mbar_arrive_expect_tx(&sh.bars[c], bytes);
+        if (bytes) bulk_load(pc.held + (b0 - pc.s0), pc.base + (size_t)b0 * V, bytes, &sh.bars[c]);
+      }
+    }
+    if (lane == 0 && q0 == 0 && q1 > 0) pc.held[0 - pc.s0] = pc.load_end(0);
+    if (lane == 0 && q0 < pc.pieces && q1 == pc.pieces)
+      pc.held[pc.pieces - 1 - pc.s0] = pc.load_end(pc.pieces - 1);
+    __syncwarp();
+  } else {
+    if (threadIdx.x < 2) pc.held[threadIdx.x] = pc.load_end(threadIdx.x ? pc.pieces - 1 : 0);
+    __syncthreads();
+  }
 
   const float t = a.temperature ? a.temperature[row] : 1.f;
   const float u = a.u[row];
@@ -789,6 +1065,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   r.min_p = r.min_p > 0.f ? fminf(r.min_p, 1.f) : 0.f;
   r.c = fminf(__fdiv_rn(kLog2e, t), 3.402823466e38f);
 
+  if constexpr (HELD) {
+    if (!mbar_wait(&sh.bars[warp / (kWarps / kChunks)], 0u)) sh.failed = 1;
+    __syncwarp();
+  }
+
   // the maximum
   float share[kShares];
 #pragma unroll
@@ -798,14 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint4 raw[kShares];
     pc.batch(b, q1, raw);
 #pragma unroll
-    for (int s = 0; s < kShares; ++s) {
-      float v[V];
-      Pieces<T>::values(raw[s], v);
-      float m = v[0];
-#pragma unroll
-      for (int j = 1; j < V; ++j) m = fmaxf(m, v[j]);
-      if (b + s * 32 + lane < q1) share[s] = fmaxf(share[s], m);
-    }
+    for (int s = 0; s < kShares; ++s)
+      if (b + s * 32 + lane < q1) share[s] = fmaxf(share[s], P::max_of(raw[s]));
   }
   float mx = fmaxf(fmaxf(share[0], share[1]), fmaxf(share[2], share[3]));
 #pragma unroll
@@ -815,18 +1090,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   mx = sh.redf[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sh.redf[w]);
-  if (threadIdx.x == 0) {
-    sh.max = mx;
-    sh.listed = 0u;
-    sh.digit = -1;
-    sh.cut = 0ull;
-    sh.sum = 0ull;
-  }
+  // (a block whose copies did not come makes the row's maximum a NaN)
+  if (threadIdx.x == 0) sh.max = HELD && sh.failed ? __int_as_float(0x7FC00000) : mx;
   team.sync();
-  team.over(&sh.max, [&](float m, int) { mx = fmaxf(mx, m); });
+  bool failed = false;
+  team.over(&sh.max, [&](float m, int) {
+    mx = fmaxf(mx, m);
+    failed = failed || m != m;
+  });
   r.top = mx;
 
-  if (mx == __int_as_float(0xFF800000)) {              // nothing left
+  if (failed || mx == __int_as_float(0xFF800000)) {    // nothing left
     if (team.rank == 0 && threadIdx.x == 0) {
       a.ids[row] = -1;
       if (a.logp) a.logp[row] = __int_as_float(0x7FC00000);
@@ -855,7 +1129,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     team.sync();
     return;
   }
-
   if (mx == __int_as_float(0x7F800000)) {
     draw_infinite(a, row, pc, q0, q1, sh, team, top_k, top_p, u);
     team.sync();
@@ -864,17 +1137,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   if (top_k > 0 && top_k <= kMaxListK) {
     // the bound: enough share maxima reach it
+    const int copy = threadIdx.x & (kCopies - 1);
 #pragma unroll
     for (int s = 0; s < kShares; ++s) {
       const float x = r.depth(share[s]);
-      if (x > -31.f) atomicAdd(&sh.count[Row::bin(x)][lane], 1u);
+      if (x > -31.f) atomicAdd(&sh.hist.count[Row::bin(x)][copy], 1u);
     }
     __syncthreads();
-    for (int d = warp; d < kBins; d += kWarps) {
-      const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, sh.count[d][lane]);
-      sh.count[d][lane] = 0u;
-      if (lane == 0) sh.bin_count[d] = c;
-    }
+    fold_hist<true, false>(sh);
     team.sync();
     u64 cnt = 0;
     if (threadIdx.x < kBins)
@@ -887,11 +1157,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // (a little below the edge, against the rounding here)
     const float bound = all ? __int_as_float(0xFF800000)
                             : r.top - ((float)sh.digit + 0.5f + 1e-3f) / (4.f * r.c);
-    pc.each(q0, q1, [&](const float (&v)[V], int i0) {
+    pc.each_above(q0, q1, bound, [&](const float (&v)[V], int i0) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (v[j] >= bound && Row::weight(Row::e(r.depth(v[j]))) != 0u)
-          append(sh, rank_key(v[j], (uint32_t)(i0 + j)));
+          append(sh, team, rank_key(v[j], (uint32_t)(i0 + j)));
     });
     team.sync();
     const u64 listed = listed_by_all(sh, team);
@@ -909,39 +1179,52 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     team.sync();                                       // counted by all before it is cleared
   }
 
-  u64 cut = 0, sum = 0;
-  if (top_k > 0) cut = find_cut<true>(pc, q0, q1, sh, team, r, top_k, 1.f, 0ull, &sum);
-  if (top_p < 1.f) cut = find_cut<false>(pc, q0, q1, sh, team, r, 0, top_p, cut, &sum);
-  if (cut != 0ull)
-    draw_in_row<true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+  u64 cut = 0;
+  if (top_k > 0) {
+    Search f;
+    f.from = 0ull;
+    f.target = (u64)top_k;
+    u64 mass;
+    cut = find_cut<true>(pc, q0, q1, sh, team, r, 1.f, f, false, &mass);
+  }
+  if (top_p < 1.f)
+    draw_nucleus(a, row, pc, q0, q1, sh, team, r, cut, top_p, u);
+  else if (cut != 0ull)
+    draw_in_row<true, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+  else if (r.min_p > 0.f)
+    draw_in_row<false, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
   else
-    draw_in_row<false>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    draw_in_row<false, false>(a, row, pc, q0, q1, sh, team, r, cut, u);
   team.sync();
 }
 
 // Blocks per row: as many as still give every row its own share of the SMs
-// (two blocks fit one), with at least 4096 logits each.
+// (two blocks fit one), with at least 4096 logits each.  (256 x 151936 bf16
+// with four blocks per row, so that shared memory holds them, took 75 us for
+// top-k and 145 us for a nucleus, most of it in the clusters' barriers.)
 int cluster_size(int m, int n) {
   int c = 1;
   while (c < kMaxCluster && 2ll * c * m <= 2ll * device_sm_count() && n / (2 * c) >= 4096) c *= 2;
   return c;
 }
 
-template <typename T>
-cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
-  const int c = cluster_size(a.m, a.n);
-  auto kern = sample_kernel<T>;
-  static bool configured = false;
-  if (!configured) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(Shared));
+template <typename T, bool HELD>
+cudaError_t launch_h(const SampleArgs& a, int c, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int slice = ((a.n + V - 1) / V + 1 + c - 1) / c + 1;     // pieces of a block, at most
+  const size_t smem = sizeof(Shared) + (size_t)(HELD ? slice : 2) * 16;
+  auto kern = sample_kernel<T, HELD>;
+  static size_t configured = 0;
+  if (smem > configured) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    configured = true;
+    configured = smem;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.m * c);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -955,6 +1238,13 @@ cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   note_launch();
   return e;
+}
+
+template <typename T>
+cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
+  const int c = cluster_size(a.m, a.n);
+  if ((size_t)a.n * sizeof(T) / c + 64 <= (size_t)kHeldBytes) return launch_h<T, true>(a, c, s);
+  return launch_h<T, false>(a, c, s);
 }
 
 }  // namespace
