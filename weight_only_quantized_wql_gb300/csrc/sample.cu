@@ -90,9 +90,19 @@ struct alignas(16) Shared {
 };
 static_assert(sizeof(Shared::hist) == kList * 12, "the joined list takes the histograms' place");
 
-__device__ __forceinline__ u64* keys(Shared& sh) { return reinterpret_cast<u64*>(&sh.hist); }
-__device__ __forceinline__ uint32_t* weights(Shared& sh) {
-  return reinterpret_cast<uint32_t*>(keys(sh) + kList);
+// Through the symbol, so that the compiler sees shared memory in functions that
+// are not inlined too (as a reference argument it made every access generic
+// and every addition to a histogram a branch).
+extern __shared__ __align__(16) uint8_t sample_smem[];
+__device__ __forceinline__ Shared& shared() { return *reinterpret_cast<Shared*>(sample_smem); }
+__device__ __forceinline__ uint4* held_pieces() {
+  return reinterpret_cast<uint4*>(sample_smem + sizeof(Shared));
+}
+
+__device__ __forceinline__ u64* keys() { return reinterpret_cast<u64*>(&shared().hist); }
+__device__ __forceinline__ uint32_t* weights() {
+  Shared& sh = shared();
+  return reinterpret_cast<uint32_t*>(keys() + kList);
 }
 
 __device__ __forceinline__ uint32_t logit_key(float l) {
@@ -151,19 +161,20 @@ struct Row {
 };
 
 // A row of logits in 16-byte pieces on 16-byte addresses: piece q holds
-// elements q*V - mis .. + V-1; those outside the row read as -inf.  HELD: this
-// block's pieces, from s0 on, are read from shared memory; otherwise only the
-// row's first and last one, which may reach outside it.
-template <typename T, bool HELD> struct Pieces {
+// elements q*V - mis .. + V-1; those outside the row read as -inf.  kHeld: this
+// block's pieces, from s0 on, are in shared memory.  kWhole: rows are whole
+// pieces in global memory.  kRagged: they may not be, and the first and the last
+// one are made up in shared memory.
+enum Mode { kHeld, kWhole, kRagged };
+template <typename T, Mode MODE> struct Pieces {
+  static constexpr bool HELD = MODE == kHeld;
   static constexpr int V = 16 / (int)sizeof(T);
   const T* base;       // 16-byte aligned, mis elements before the row
-  uint4* held;
   int mis, n, pieces, s0;
-  __device__ __forceinline__ Pieces(const T* row, int n_, uint8_t* smem) : n(n_) {
+  __device__ __forceinline__ Pieces(const T* row, int n_) : n(n_) {
     mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     base = row - mis;
     pieces = (n + mis + V - 1) / V;
-    held = reinterpret_cast<uint4*>(smem);
     s0 = 0;
   }
   // first piece of a warp's part
@@ -176,12 +187,12 @@ template <typename T, bool HELD> struct Pieces {
   }
   __device__ __forceinline__ uint4 load(int q) const {
     if constexpr (HELD) {
-      return held[q - s0];
+      return held_pieces()[q - s0];
     } else {
-      const uint4* p = reinterpret_cast<const uint4*>(base) + q;
-      if (q == 0) p = held;                  // the ends, made up in shared memory
-      if (q == pieces - 1) p = held + 1;
-      return *p;
+      if constexpr (MODE == kRagged) {
+        if (q == 0 || q == pieces - 1) return held_pieces()[q == 0 ? 0 : 1];
+      }
+      return __ldg(reinterpret_cast<const uint4*>(base) + q);
     }
   }
   // the first or last piece, element by element
@@ -229,30 +240,27 @@ template <typename T, bool HELD> struct Pieces {
       r[u] = q < q1 ? load(q) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  // f(piece, its number) for this warp's pieces q0 .. q1, one a turn
-  template <typename F> __device__ __forceinline__ void each_piece(int q0, int q1, F f) const {
+  // f(piece, its number, turn) for this warp's pieces q0 .. q1: one a turn, the
+  // loads of the next D - 1 in flight; turn = 0 .. D-1
+  template <int D, typename F>
+  __device__ __forceinline__ void each_piece(int q0, int q1, F f) const {
     int q = q0 + (int)(threadIdx.x & 31);
-    if constexpr (HELD) {
+    uint4 r[D];
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      if (q + u * 32 < q1) r[u] = load(q + u * 32);
 #pragma unroll 1
-      for (; q < q1; q += 32) f(load(q), q);
-    } else {
-      uint4 r0, r1, r2;               // the next three pieces in flight
-      if (q < q1) r0 = load(q);
-      if (q + 32 < q1) r1 = load(q + 32);
-      if (q + 64 < q1) r2 = load(q + 64);
-#pragma unroll 1
-      for (; q < q1; q += 32) {
-        const uint4 r = r0;
-        r0 = r1;
-        r1 = r2;
-        if (q + 96 < q1) r2 = load(q + 96);
-        f(r, q);
+    for (; q < q1; q += 32 * D) {
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        if (q + u * 32 < q1) f(r[u], q + u * 32, u);
+        if (q + (u + D) * 32 < q1) r[u] = load(q + (u + D) * 32);
       }
     }
   }
   // f(values, index of the first) for them
   template <typename F> __device__ __forceinline__ void each(int q0, int q1, F f) const {
-    each_piece(q0, q1, [&](const uint4& r, int q) {
+    each_piece<HELD ? 1 : 3>(q0, q1, [&](const uint4& r, int q, int) {
       float v[V];
       values(r, v);
       f(v, q * V - mis);
@@ -261,7 +269,7 @@ template <typename T, bool HELD> struct Pieces {
   // and for those whose largest value reaches `low`
   template <typename F>
   __device__ __forceinline__ void each_above(int q0, int q1, float low, F f) const {
-    each_piece(q0, q1, [&](const uint4& r, int q) {
+    each_piece<HELD ? 1 : 3>(q0, q1, [&](const uint4& r, int q, int) {
       if (max_of(r) >= low) {
         float v[V];
         values(r, v);
@@ -315,7 +323,8 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {      // inclusive
 }
 
 // Exclusive prefix sum over the block; *total gets the sum.
-__device__ u64 block_scan(u64 v, Shared& sh, u64* total) {
+__device__ u64 block_scan(u64 v, u64* total) {
+  Shared& sh = shared();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const u64 inc = warp_scan(v);
   __syncthreads();
@@ -333,17 +342,18 @@ __device__ u64 block_scan(u64 v, Shared& sh, u64* total) {
 }
 
 // Sorts the joined list's first `size` keys descending; a power of two, at least 2.
-__device__ void sort_list(Shared& sh, int size) {
+__device__ void sort_list(int size) {
+  Shared& sh = shared();
   __syncthreads();
   for (int len = 2; len <= size; len <<= 1) {
     for (int stride = len >> 1; stride > 0; stride >>= 1) {
       for (int i = threadIdx.x; i < size / 2; i += kThreads) {
         const int p = 2 * i - (i & (stride - 1));
-        const u64 a = keys(sh)[p], b = keys(sh)[p + stride];
+        const u64 a = keys()[p], b = keys()[p + stride];
         const bool up = (p & len) != 0;              // ascending stretch
         if (up ? a > b : a < b) {
-          keys(sh)[p] = b;
-          keys(sh)[p + stride] = a;
+          keys()[p] = b;
+          keys()[p + stride] = a;
         }
       }
       // a warp's pairs of strides <= 32 stay within its own 64 entries
@@ -363,18 +373,21 @@ __device__ __forceinline__ int pow2_at_least(int v) {
 }
 
 // A block's own list; a block alone fills the joined one.
-__device__ __forceinline__ u64* own_list(Shared& sh, const Team& team) {
-  return team.size > 1 ? sh.list : keys(sh);
+__device__ __forceinline__ u64* own_list(const Team& team) {
+  Shared& sh = shared();
+  return team.size > 1 ? sh.list : keys();
 }
-__device__ __forceinline__ void append(Shared& sh, const Team& team, u64 key) {
+__device__ __forceinline__ void append(const Team& team, u64 key) {
+  Shared& sh = shared();
   const uint32_t at = atomicAdd(&sh.listed, 1u);
-  if (at < (uint32_t)(team.size > 1 ? kLocal : kList)) own_list(sh, team)[at] = key;
+  if (at < (uint32_t)(team.size > 1 ? kLocal : kList)) own_list(team)[at] = key;
 }
 
 // Tokens listed by all blocks of the cluster; more than kList when they do not
 // fit.  After a sync that follows the gathering; the caller syncs before the
 // lists are used again.
-__device__ __forceinline__ u64 listed_by_all(Shared& sh, const Team& team) {
+__device__ __forceinline__ u64 listed_by_all(const Team& team) {
+  Shared& sh = shared();
   if (team.size == 1) return sh.listed;
   u64 total = 0;
   team.over(&sh.listed, [&](uint32_t c, int) {
@@ -384,7 +397,8 @@ __device__ __forceinline__ u64 listed_by_all(Shared& sh, const Team& team) {
 }
 
 // The first block's joined list gets all blocks' lists (they fit).
-__device__ void join_lists(Shared& sh, const Team& team) {
+__device__ void join_lists(const Team& team) {
+  Shared& sh = shared();
   if (team.rank != 0 || team.size == 1) return;
   const int warp = threadIdx.x >> 5;                   // one warp a block's list
   if (warp < team.size) {
@@ -394,7 +408,7 @@ __device__ void join_lists(Shared& sh, const Team& team) {
       if (k == warp) mine = c;
     });
     const u64* src = team.of(&sh.list[0], warp);
-    for (uint32_t i = threadIdx.x & 31; i < mine; i += 32) keys(sh)[at + i] = src[i];
+    for (uint32_t i = threadIdx.x & 31; i < mine; i += 32) keys()[at + i] = src[i];
   }
   __syncthreads();
 }
@@ -422,39 +436,40 @@ __device__ __forceinline__ void write_draw(const SampleArgs& a, int row, int id,
 // joined list, which hold the first top_k by rank (or, fewer, all with a weight).
 // Short lists: every token counts the tokens and sums the weights before it,
 // by rank and then, among the kept, by index.
-__device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Shared& sh,
+__device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row,
                                                 const Row& r, int len, int top_k, float top_p,
                                                 float u) {
+  Shared& sh = shared();
   static_assert(kThreads == 4 * kCountRank, "four lanes a token");
   const int p = threadIdx.x >> 2, part = threadIdx.x & 3;
   u64 key = 0;
   float e = 0.f;
   uint32_t w = 0;
   if (p < len) {
-    key = keys(sh)[p];
+    key = keys()[p];
     e = Row::e(r.depth(rank_logit(key)));
     w = Row::weight(e);
-    if (part == 0) weights(sh)[p] = w;
+    if (part == 0) weights()[p] = w;
   }
   __syncthreads();
   u64 before = 0;                      // weights before it by rank, and how many tokens
   for (int j = part; j < len; j += 4)
-    if (keys(sh)[j] > key) before += ((u64)weights(sh)[j] << 8) | 1u;
+    if (keys()[j] > key) before += ((u64)weights()[j] << 8) | 1u;
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
   const bool in_k = p < len && (int)(before & 255u) < top_k;
   before >>= 8;
   u64 sum = ~0ull;
-  if (top_p < 1.f) block_scan(in_k && part == 0 ? w : 0u, sh, &sum);
+  if (top_p < 1.f) block_scan(in_k && part == 0 ? w : 0u, &sum);
   const bool keep = in_k && (top_p >= 1.f || before < nucleus_target(top_p, sum)) && e >= r.min_p;
   u64 kept;
-  block_scan(keep && part == 0 ? w : 0u, sh, &kept);
-  if (p < len && !keep && part == 0) weights(sh)[p] = 0u;
+  block_scan(keep && part == 0 ? w : 0u, &kept);
+  if (p < len && !keep && part == 0) weights()[p] = 0u;
   __syncthreads();
   u64 run = 0;                         // kept weights of lower indices
   const uint32_t idx = rank_index(key);
   for (int j = part; j < len; j += 4)
-    if (rank_index(keys(sh)[j]) < idx) run += weights(sh)[j];
+    if (rank_index(keys()[j]) < idx) run += weights()[j];
   run += __shfl_xor_sync(0xFFFFFFFFu, run, 1);
   run += __shfl_xor_sync(0xFFFFFFFFu, run, 2);
   const u64 target = draw_target(u, kept);
@@ -463,11 +478,12 @@ __device__ __noinline__ void finish_by_counting(const SampleArgs& a, int row, Sh
 }
 
 // The same for longer lists: sort, prefix sums, sort the kept by index.
-__device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Shared& sh, const Row& r, int len,
+__device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, const Row& r, int len,
                                   int top_k, float top_p, float u) {
+  Shared& sh = shared();
   const int size = pow2_at_least(len);
-  for (int i = len + threadIdx.x; i < size; i += kThreads) keys(sh)[i] = 0ull;
-  sort_list(sh, size);
+  for (int i = len + threadIdx.x; i < size; i += kThreads) keys()[i] = 0ull;
+  sort_list(size);
   constexpr int kPer = kList / kThreads;
   const int per = (size + kThreads - 1) / kThreads;    // 1..kPer consecutive entries a thread
   float e[kPer];
@@ -480,13 +496,13 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
     w[i] = 0u;
     e[i] = 0.f;
     if (i < per && p < limit) {
-      e[i] = Row::e(r.depth(rank_logit(keys(sh)[p])));
+      e[i] = Row::e(r.depth(rank_logit(keys()[p])));
       w[i] = Row::weight(e[i]);
       mine += w[i];
     }
   }
   u64 sum;
-  u64 before = block_scan(mine, sh, &sum);
+  u64 before = block_scan(mine, &sum);
   const u64 reach = top_p < 1.f ? nucleus_target(top_p, sum) : ~0ull;
   // keep a prefix: count it, and its weights
   u64 kept = 0;
@@ -496,10 +512,10 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
     if (i < per && p < limit && before < reach && e[i] >= r.min_p)
       kept += ((u64)w[i] << 12) | 1u;                  // up to 2^11 weights of 2^31, and a count
     before += w[i];
-    if (i < per && p < kList) weights(sh)[p] = w[i];
+    if (i < per && p < kList) weights()[p] = w[i];
   }
   u64 kept_total;
-  block_scan(kept, sh, &kept_total);
+  block_scan(kept, &kept_total);
   const int keep = (int)(kept_total & 0xFFFu);
   const u64 kept_sum = kept_total >> 12;
   // the kept tokens by index: (inverted index, rank), descending
@@ -508,41 +524,43 @@ __device__ __noinline__ void finish_by_sorting(const SampleArgs& a, int row, Sha
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x + i * kThreads;
-    by_index[i] = p < keep ? ((keys(sh)[p] & kIndexMask) << 32) | (u64)p : 0ull;
+    by_index[i] = p < keep ? ((keys()[p] & kIndexMask) << 32) | (u64)p : 0ull;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x + i * kThreads;
-    if (p < size2) keys(sh)[p] = by_index[i];
+    if (p < size2) keys()[p] = by_index[i];
   }
-  sort_list(sh, size2);
+  sort_list(size2);
   const int per2 = (size2 + kThreads - 1) / kThreads;
   mine = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int p = threadIdx.x * per2 + i;
-    w[i] = (i < per2 && p < keep) ? weights(sh)[(uint32_t)keys(sh)[p]] : 0u;
+    w[i] = (i < per2 && p < keep) ? weights()[(uint32_t)keys()[p]] : 0u;
     mine += w[i];
   }
-  before = block_scan(mine, sh, &sum);
+  before = block_scan(mine, &sum);
   const u64 target = draw_target(u, kept_sum);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (before <= target && target < before + w[i])
-      write_draw(a, row, (int)(~(uint32_t)(keys(sh)[threadIdx.x * per2 + i] >> 32) & kIndexMask),
+      write_draw(a, row, (int)(~(uint32_t)(keys()[threadIdx.x * per2 + i] >> 32) & kIndexMask),
                  w[i], kept_sum);
     before += w[i];
   }
 }
 
-__device__ __forceinline__ void clear_hist(Shared& sh) {
+__device__ __forceinline__ void clear_hist() {
+  Shared& sh = shared();
   uint32_t* h = &sh.hist.low[0][0];      // low, high, count
   for (int i = threadIdx.x; i < 3 * kBins * kCopies; i += kThreads) h[i] = 0u;
 }
 
 // Folds the copies of the histograms into bin_mass and bin_count.
-template <bool COUNT, bool MASS> __device__ __forceinline__ void fold_hist(Shared& sh) {
+template <bool COUNT, bool MASS> __device__ __forceinline__ void fold_hist() {
+  Shared& sh = shared();
   const int copy = threadIdx.x & (kCopies - 1);
   for (int d = threadIdx.x / kCopies; d < kBins; d += kThreads / kCopies) {
     u64 m = MASS ? (u64)sh.hist.low[d][copy] + ((u64)sh.hist.high[d][copy] << 16) : 0ull;
@@ -557,6 +575,17 @@ template <bool COUNT, bool MASS> __device__ __forceinline__ void fold_hist(Share
       if (COUNT) sh.bin_count[d] = c;
     }
   }
+}
+
+// An addition in shared memory under a predicate (an if around atomicAdd()
+// becomes a branch per token).
+__device__ __forceinline__ void add_if(bool yes, uint32_t addr, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p red.shared.add.u32 [%0], %1;\n\t}" ::"r"(addr),
+      "r"(v), "r"((uint32_t)yes)
+      : "memory");
 }
 
 // Where a row's cut is being looked for.
@@ -575,15 +604,16 @@ struct Search {
 // target follows from the first histogram, whose total is the sum of all
 // weights.  False when the total stays below the target; *total_mass gets it.
 template <bool COUNT, typename P>
-__device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& sh,
+__device__ __noinline__ bool search_round(const P& pc, int q0, int q1,
                                           const Team& team, const Row& r, float top_p, Search& f,
                                           u64* total_mass) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   constexpr int kDigitBits = 7;
   const int copy = threadIdx.x & (kCopies - 1);
   const bool first = f.bin < 0;
   const int dshift = first ? f.shift : f.shift - kDigitBits;
-  clear_hist(sh);
+  clear_hist();
   if (threadIdx.x == 0) {
     sh.digit = -1;
     sh.listed = 0u;
@@ -591,6 +621,7 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& s
   __syncthreads();
   constexpr int kHigh = kBins * kCopies, kCount = 2 * kHigh;     // from a low sum to the others
   uint32_t* const hist = &sh.hist.low[0][copy];
+  const uint32_t hist_addr = smem_u32(hist);
   if (first && f.from == 0ull) {
     pc.each(q0, q1, [&](const float (&v)[V], int) {
 #pragma unroll
@@ -598,10 +629,10 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& s
         const float x = r.depth(v[j]);
         uint32_t high, low;
         Row::halves(Row::e(x), &high, &low);
-        uint32_t* h = hist + Row::bin_if_weight(x) * kCopies;
-        if (x > -31.5f) atomicAdd(h, low - Row::kOne);
-        if (high != Row::kOne) atomicAdd(h + kHigh, high - Row::kOne);
-        if (COUNT && (high | low) != Row::kOne) atomicAdd(h + kCount, 1u);
+        const uint32_t h = hist_addr + Row::bin_if_weight(x) * (kCopies * 4);
+        add_if(x > -31.5f, h, low - Row::kOne);
+        add_if(high != Row::kOne, h + kHigh * 4, high - Row::kOne);
+        if (COUNT) add_if((high | low) != Row::kOne, h + kCount * 4, 1u);
       }
     });
   } else {
@@ -628,7 +659,7 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& s
     });
   }
   __syncthreads();
-  fold_hist<COUNT, true>(sh);
+  fold_hist<COUNT, true>();
   team.sync();
   // every block joins the histograms and comes to the same choice
   u64 cnt = 0, mass = 0;
@@ -637,8 +668,8 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1, Shared& s
     if (COUNT) team.over(&sh.bin_count[threadIdx.x], [&](uint32_t c, int) { cnt += c; });
   }
   u64 total, total_count;
-  const u64 to_mass = f.before_mass + block_scan(mass, sh, &total);
-  const u64 to_count = COUNT ? f.before_count + block_scan(cnt, sh, &total_count) : 0ull;
+  const u64 to_mass = f.before_mass + block_scan(mass, &total);
+  const u64 to_count = COUNT ? f.before_count + block_scan(cnt, &total_count) : 0ull;
   *total_mass = total;
   if (!COUNT && first) f.target = nucleus_target(top_p, total);
   const u64 lo = COUNT ? to_count : to_mass, hi = lo + (COUNT ? cnt : mass);
@@ -674,23 +705,24 @@ __device__ __forceinline__ float bin_high(const Row& r, int bin) {
 // one at which the target is reached, and (*mass) the weights up to it.
 // Ends with a sync.
 template <bool COUNT>
-__device__ __noinline__ u64 rank_open(Shared& sh, const Team& team, const Row& r, const Search& f,
+__device__ __noinline__ u64 rank_open(const Team& team, const Row& r, const Search& f,
                                       int len, u64* mass_out) {
-  join_lists(sh, team);
+  Shared& sh = shared();
+  join_lists(team);
   if (team.rank == 0) {
     if (len <= kCountRank) {
       const int p = threadIdx.x >> 2, part = threadIdx.x & 3;
       u64 key = 0;
       uint32_t w = 0;
       if (p < len) {
-        key = keys(sh)[p];
+        key = keys()[p];
         w = Row::weight(Row::e(r.depth(rank_logit(key))));
-        if (part == 0) weights(sh)[p] = w;
+        if (part == 0) weights()[p] = w;
       }
       __syncthreads();
       u64 ahead = 0;
       for (int j = part; j < len; j += 4)
-        if (keys(sh)[j] > key) ahead += ((u64)weights(sh)[j] << 8) | 1u;
+        if (keys()[j] > key) ahead += ((u64)weights()[j] << 8) | 1u;
       ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, 1);
       ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, 2);
       const u64 mass = f.before_mass + (ahead >> 8);
@@ -702,24 +734,24 @@ __device__ __noinline__ u64 rank_open(Shared& sh, const Team& team, const Row& r
       }
     } else {
       const int size = pow2_at_least(len);
-      for (int i = len + threadIdx.x; i < size; i += kThreads) keys(sh)[i] = 0ull;
-      sort_list(sh, size);
+      for (int i = len + threadIdx.x; i < size; i += kThreads) keys()[i] = 0ull;
+      sort_list(size);
       const int per = (size + kThreads - 1) / kThreads;    // consecutive entries a thread
       const int p0 = threadIdx.x * per, p1 = min(p0 + per, len);
       u64 mine = 0;
       for (int p = p0; p < p1; ++p) {
-        const uint32_t w = Row::weight(Row::e(r.depth(rank_logit(keys(sh)[p]))));
-        weights(sh)[p] = w;
+        const uint32_t w = Row::weight(Row::e(r.depth(rank_logit(keys()[p]))));
+        weights()[p] = w;
         mine += w;
       }
       u64 total;
-      u64 mass = f.before_mass + block_scan(mine, sh, &total);
+      u64 mass = f.before_mass + block_scan(mine, &total);
       for (int p = p0; p < p1; ++p) {
-        const uint32_t w = weights(sh)[p];
+        const uint32_t w = weights()[p];
         const u64 lo = COUNT ? f.before_count + (u64)p : mass;
         const u64 hi = lo + (COUNT ? 1ull : (u64)w);
         if (lo < f.target && f.target <= hi) {
-          sh.cut = keys(sh)[p];
+          sh.cut = keys()[p];
           sh.sum = mass + w;
         }
         mass += w;
@@ -737,12 +769,13 @@ __device__ __noinline__ u64 rank_open(Shared& sh, const Team& team, const Row& r
 // search's target; 0 when all tokens together do not.  *mass_out gets the
 // prefix's sum of weights.  `f` may have its first round behind it (`started`).
 template <bool COUNT, typename P>
-__device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, Shared& sh, const Team& team,
+__device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, const Team& team,
                                      const Row& r, float top_p, Search& f, bool started,
                                      u64* mass_out) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   for (;;) {
-    if (!started && !search_round<COUNT>(pc, q0, q1, sh, team, r, top_p, f, mass_out)) {
+    if (!started && !search_round<COUNT>(pc, q0, q1, team, r, top_p, f, mass_out)) {
       team.sync();
       return 0ull;
     }
@@ -757,12 +790,12 @@ __device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, Shared& sh, co
             const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
             if (Row::weight(Row::e(x)) != 0u && Row::bin(x) == f.bin && key >= f.from &&
                 (key >> f.shift) == f.prefix)
-              append(sh, team, key);
+              append(team, key);
           }
       });
       team.sync();
-      const u64 open = listed_by_all(sh, team);
-      if (open <= (u64)kList) return rank_open<COUNT>(sh, team, r, f, (int)open, mass_out);
+      const u64 open = listed_by_all(team);
+      if (open <= (u64)kList) return rank_open<COUNT>(team, r, f, (int)open, mass_out);
     }
     started = false;
     team.sync();                       // counted by all before the next round clears
@@ -773,8 +806,9 @@ __device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, Shared& sh, co
 // batches each; among tokens with e >= min_p and (CUT) a rank key >= `cut`.
 template <bool CUT, typename P>
 __device__ __noinline__ void draw_by_stretch(const SampleArgs& a, int row, const P& pc, int q0,
-                                             int q1, int per, Shared& sh, const Team& team,
+                                             int q1, int per, const Team& team,
                                              const Row& r, u64 cut, float u) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   constexpr int kBatch = 32 * kShares;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -847,7 +881,8 @@ __device__ __forceinline__ int batches_per_stretch(int q0, int q1) {
 // f(first piece, one past the last) -> this lane's sum, for every stretch of
 // this warp; the warp's sums go to sh.seg.
 template <typename F>
-__device__ __forceinline__ void sum_stretches(int q0, int q1, int per, Shared& sh, F f) {
+__device__ __forceinline__ void sum_stretches(int q0, int q1, int per, F f) {
+  Shared& sh = shared();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int step = per * 32 * kShares;
   int seg = 0;
@@ -861,12 +896,13 @@ __device__ __forceinline__ void sum_stretches(int q0, int q1, int per, Shared& s
 // and (CUT) a rank key of at least `cut`.
 template <bool CUT, bool MIN_P, typename P>
 __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& pc, int q0, int q1,
-                                         Shared& sh, const Team& team, const Row& r, u64 cut,
+                                         const Team& team, const Row& r, u64 cut,
                                          float u) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   const float lowest = rank_logit(cut);
   const int per = batches_per_stretch(q0, q1);
-  sum_stretches(q0, q1, per, sh, [&](int b0, int b1) {
+  sum_stretches(q0, q1, per, [&](int b0, int b1) {
     u64 mine = 0;
     if constexpr (CUT) {
       pc.each_above(b0, b1, lowest, [&](const float (&v)[V], int i0) {
@@ -901,23 +937,24 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
     return mine;
   });
   __syncthreads();
-  draw_by_stretch<CUT>(a, row, pc, q0, q1, per, sh, team, r, cut, u);
+  draw_by_stretch<CUT>(a, row, pc, q0, q1, per, team, r, cut, u);
 }
 
 // A nucleus (within the tokens of rank key >= from) and the draw in it.
 template <typename P>
 __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P& pc, int q0,
-                                          int q1, Shared& sh, const Team& team, const Row& r,
+                                          int q1, const Team& team, const Row& r,
                                           u64 from, float top_p, float u) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   Search f;
   f.from = from;
   u64 mass;
   // (always found: the largest weight is 2^31)
-  search_round<false>(pc, q0, q1, sh, team, r, top_p, f, &mass);
+  search_round<false>(pc, q0, q1, team, r, top_p, f, &mass);
   const float low = bin_low(r, f.bin);
   const int per = batches_per_stretch(q0, q1);
-  sum_stretches(q0, q1, per, sh, [&](int b0, int b1) {
+  sum_stretches(q0, q1, per, [&](int b0, int b1) {
     u64 mine = 0;
     pc.each_above(b0, b1, low, [&](const float (&v)[V], int i0) {
 #pragma unroll
@@ -931,24 +968,24 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
           mine += e >= r.min_p ? w : 0u;           // above the open ones: kept
         } else if (b == f.bin && w != 0u) {
           const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
-          if (key >= from) append(sh, team, key);
+          if (key >= from) append(team, key);
         }
       }
     });
     return mine;
   });
   team.sync();
-  const u64 open = listed_by_all(sh, team);
+  const u64 open = listed_by_all(team);
   if (open > (u64)kList) {
-    const u64 cut = find_cut<false>(pc, q0, q1, sh, team, r, top_p, f, true, &mass);
-    draw_in_row<true, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    const u64 cut = find_cut<false>(pc, q0, q1, team, r, top_p, f, true, &mass);
+    draw_in_row<true, true>(a, row, pc, q0, q1, team, r, cut, u);
     return;
   }
-  const u64 cut = rank_open<false>(sh, team, r, f, (int)open, &mass);
+  const u64 cut = rank_open<false>(team, r, f, (int)open, &mass);
   // this block's open tokens that are kept join their stretches' sums
   const int parts = team.size * kWarps;
   for (int i = threadIdx.x; i < (int)sh.listed; i += kThreads) {
-    const u64 key = own_list(sh, team)[i];
+    const u64 key = own_list(team)[i];
     const float e = Row::e(r.depth(rank_logit(key)));
     if (key < cut || !(e >= r.min_p)) continue;
     const int q = ((int)rank_index(key) + pc.mis) / V;
@@ -958,15 +995,16 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
     atomicAdd(&sh.seg[part - team.rank * kWarps][seg], (u64)Row::weight(e));
   }
   __syncthreads();
-  draw_by_stretch<true>(a, row, pc, q0, q1, per, sh, team, r, cut, u);
+  draw_by_stretch<true>(a, row, pc, q0, q1, per, team, r, cut, u);
 }
 
 // A row whose maximum is +inf: the infinite logits share the draw, a weight
 // of 2^31 each, ranked by index.
 template <typename P>
 __device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P& pc,
-                                           int q0, int q1, Shared& sh, const Team& team, int top_k,
+                                           int q0, int q1, const Team& team, int top_k,
                                            float top_p, float u) {
+  Shared& sh = shared();
   constexpr int V = P::V;
   const int lane = threadIdx.x & 31;
   const float inf = __int_as_float(0x7F800000);
@@ -977,7 +1015,7 @@ __device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P
   });
   const u64 warp_total = warp_sum(mine);
   u64 total;
-  u64 before = block_scan(lane == 0 ? warp_total : 0ull, sh, &total);   // of lane 0
+  u64 before = block_scan(lane == 0 ? warp_total : 0ull, &total);   // of lane 0
   before = __shfl_sync(0xFFFFFFFFu, before, 0);
   if (threadIdx.x == 0) sh.sum = total;
   team.sync();
@@ -1005,16 +1043,16 @@ __device__ __noinline__ void draw_infinite(const SampleArgs& a, int row, const P
   }
 }
 
-template <typename T, bool HELD>
+template <typename T, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
-  using P = Pieces<T, HELD>;
+  Shared& sh = shared();
+  using P = Pieces<T, MODE>;
+  constexpr bool HELD = P::HELD;
   constexpr int V = P::V;
   const Team team;
   const int row = blockIdx.x / team.size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  P pc(reinterpret_cast<const T*>(a.logits) + (size_t)row * a.n, a.n, smem + sizeof(Shared));
+  P pc(reinterpret_cast<const T*>(a.logits) + (size_t)row * a.n, a.n);
   // this warp's pieces
   const int parts = team.size * kWarps, part = team.rank * kWarps + warp;
   const int q0 = pc.first(part, parts), q1 = pc.first(part + 1, parts);
@@ -1028,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sh.sum = 0ull;
     fence_barrier_init();
   }
-  clear_hist(sh);
+  clear_hist();
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
@@ -1042,15 +1080,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const int b1 = min(pc.first(w0 + kWarps / kChunks, parts), pc.pieces - 1);
         const uint32_t bytes = b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
         mbar_arrive_expect_tx(&sh.bars[c], bytes);
-        if (bytes) bulk_load(pc.held + (b0 - pc.s0), pc.base + (size_t)b0 * V, bytes, &sh.bars[c]);
+        if (bytes) bulk_load(held_pieces() + (b0 - pc.s0), pc.base + (size_t)b0 * V, bytes, &sh.bars[c]);
       }
     }
-    if (lane == 0 && q0 == 0 && q1 > 0) pc.held[0 - pc.s0] = pc.load_end(0);
+    if (lane == 0 && q0 == 0 && q1 > 0) held_pieces()[0 - pc.s0] = pc.load_end(0);
     if (lane == 0 && q0 < pc.pieces && q1 == pc.pieces)
-      pc.held[pc.pieces - 1 - pc.s0] = pc.load_end(pc.pieces - 1);
+      held_pieces()[pc.pieces - 1 - pc.s0] = pc.load_end(pc.pieces - 1);
     __syncwarp();
-  } else {
-    if (threadIdx.x < 2) pc.held[threadIdx.x] = pc.load_end(threadIdx.x ? pc.pieces - 1 : 0);
+  } else if constexpr (MODE == kRagged) {
+    if (threadIdx.x < 2) held_pieces()[threadIdx.x] = pc.load_end(threadIdx.x ? pc.pieces - 1 : 0);
     __syncthreads();
   }
 
@@ -1074,14 +1112,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   float share[kShares];
 #pragma unroll
   for (int s = 0; s < kShares; ++s) share[s] = __int_as_float(0xFF800000);
-#pragma unroll 1
-  for (int b = q0; b < q1; b += 32 * kShares) {
-    uint4 raw[kShares];
-    pc.batch(b, q1, raw);
-#pragma unroll
-    for (int s = 0; s < kShares; ++s)
-      if (b + s * 32 + lane < q1) share[s] = fmaxf(share[s], P::max_of(raw[s]));
-  }
+  pc.template each_piece<kShares>(q0, q1, [&](const uint4& piece, int, int s) {
+    share[s] = fmaxf(share[s], P::max_of(piece));
+  });
   float mx = fmaxf(fmaxf(share[0], share[1]), fmaxf(share[2], share[3]));
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, m));
@@ -1130,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return;
   }
   if (mx == __int_as_float(0x7F800000)) {
-    draw_infinite(a, row, pc, q0, q1, sh, team, top_k, top_p, u);
+    draw_infinite(a, row, pc, q0, q1, team, top_k, top_p, u);
     team.sync();
     return;
   }
@@ -1144,13 +1177,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (x > -31.f) atomicAdd(&sh.hist.count[Row::bin(x)][copy], 1u);
     }
     __syncthreads();
-    fold_hist<true, false>(sh);
+    fold_hist<true, false>();
     team.sync();
     u64 cnt = 0;
     if (threadIdx.x < kBins)
       team.over(&sh.bin_count[threadIdx.x], [&](uint32_t c, int) { cnt += c; });
     u64 total;
-    const u64 below = block_scan(cnt, sh, &total);
+    const u64 below = block_scan(cnt, &total);
     if (below < (u64)top_k && (u64)top_k <= below + cnt) sh.digit = (int)threadIdx.x;
     __syncthreads();
     const bool all = sh.digit < 0;
@@ -1161,17 +1194,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (v[j] >= bound && Row::weight(Row::e(r.depth(v[j]))) != 0u)
-          append(sh, team, rank_key(v[j], (uint32_t)(i0 + j)));
+          append(team, rank_key(v[j], (uint32_t)(i0 + j)));
     });
     team.sync();
-    const u64 listed = listed_by_all(sh, team);
+    const u64 listed = listed_by_all(team);
     if (listed <= (u64)kList && (all || listed >= (u64)top_k)) {
-      join_lists(sh, team);
+      join_lists(team);
       if (team.rank == 0) {
         if (listed <= (u64)kCountRank)
-          finish_by_counting(a, row, sh, r, (int)listed, top_k, top_p, u);
+          finish_by_counting(a, row, r, (int)listed, top_k, top_p, u);
         else
-          finish_by_sorting(a, row, sh, r, (int)listed, top_k, top_p, u);
+          finish_by_sorting(a, row, r, (int)listed, top_k, top_p, u);
       }
       team.sync();
       return;
@@ -1185,16 +1218,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     f.from = 0ull;
     f.target = (u64)top_k;
     u64 mass;
-    cut = find_cut<true>(pc, q0, q1, sh, team, r, 1.f, f, false, &mass);
+    cut = find_cut<true>(pc, q0, q1, team, r, 1.f, f, false, &mass);
   }
   if (top_p < 1.f)
-    draw_nucleus(a, row, pc, q0, q1, sh, team, r, cut, top_p, u);
+    draw_nucleus(a, row, pc, q0, q1, team, r, cut, top_p, u);
   else if (cut != 0ull)
-    draw_in_row<true, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    draw_in_row<true, true>(a, row, pc, q0, q1, team, r, cut, u);
   else if (r.min_p > 0.f)
-    draw_in_row<false, true>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    draw_in_row<false, true>(a, row, pc, q0, q1, team, r, cut, u);
   else
-    draw_in_row<false, false>(a, row, pc, q0, q1, sh, team, r, cut, u);
+    draw_in_row<false, false>(a, row, pc, q0, q1, team, r, cut, u);
   team.sync();
 }
 
@@ -1208,12 +1241,12 @@ int cluster_size(int m, int n) {
   return c;
 }
 
-template <typename T, bool HELD>
+template <typename T, Mode MODE>
 cudaError_t launch_h(const SampleArgs& a, int c, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const int slice = ((a.n + V - 1) / V + 1 + c - 1) / c + 1;     // pieces of a block, at most
-  const size_t smem = sizeof(Shared) + (size_t)(HELD ? slice : 2) * 16;
-  auto kern = sample_kernel<T, HELD>;
+  const size_t smem = sizeof(Shared) + (size_t)(MODE == kHeld ? slice : 2) * 16;
+  auto kern = sample_kernel<T, MODE>;
   static size_t configured = 0;
   if (smem > configured) {
     const cudaError_t e =
@@ -1243,8 +1276,9 @@ cudaError_t launch_h(const SampleArgs& a, int c, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
   const int c = cluster_size(a.m, a.n);
-  if ((size_t)a.n * sizeof(T) / c + 64 <= (size_t)kHeldBytes) return launch_h<T, true>(a, c, s);
-  return launch_h<T, false>(a, c, s);
+  if ((size_t)a.n * sizeof(T) / c + 64 <= (size_t)kHeldBytes) return launch_h<T, kHeld>(a, c, s);
+  if (a.n % (16 / (int)sizeof(T)) == 0) return launch_h<T, kWhole>(a, c, s);
+  return launch_h<T, kRagged>(a, c, s);
 }
 
 }  // namespace
