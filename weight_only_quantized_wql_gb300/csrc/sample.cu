@@ -33,6 +33,7 @@
 // partner, so that a warp's additions hardly meet in a bank; a copy's sums (16
 // low and 15 high bits of the weights apart) stay below 2^32 for 2^20 tokens.
 #include <cooperative_groups.h>
+#include <stddef.h>
 
 #include <type_traits>
 
@@ -48,7 +49,8 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 2048;          // tokens the joined list holds
+constexpr int kList = 2048;          // tokens the joined list holds with their weights
+constexpr int kOpen = 4096;          // and without
 constexpr int kLocal = 1024;         // a block's own list, in a cluster
 constexpr int kBins = 128;
 constexpr int kCopies = 16;          // of a histogram
@@ -64,7 +66,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 static_assert(WQL_SAMPLE_MAX_N == 1 << kIndexBits, "rank keys hold an index");
 
 struct alignas(16) Shared {
-  u64 list[kLocal];
   u64 seg[kWarps][kSegs];
   u64 red[kWarps];
   float redf[kWarps];
@@ -80,15 +81,19 @@ struct alignas(16) Shared {
   // block-wide results
   int digit;
   u64 before_count, before_mass;
-  // histograms; once they are folded, the joined list takes their place: kList
-  // keys, then their weights
-  struct alignas(16) {
+  // this block's list; in the first block, the joined one, which goes on where
+  // the histograms are, once they are folded: kOpen rank keys, or kList and
+  // their weights
+  u64 list[kLocal];
+  struct {
     uint32_t low[kBins][kCopies];      // sums of weights' low 16 bits
     uint32_t high[kBins][kCopies];     // and of the bits above
     uint32_t count[kBins][kCopies];
   } hist;
 };
-static_assert(sizeof(Shared::hist) == kList * 12, "the joined list takes the histograms' place");
+static_assert(offsetof(Shared, hist) == offsetof(Shared, list) + kLocal * 8 &&
+                  sizeof(Shared::hist) >= (kOpen - kLocal) * 8 && kList * 12 <= kOpen * 8,
+              "the joined list goes on into the histograms");
 
 // Through the symbol, so that the compiler sees shared memory in functions that
 // are not inlined too (as a reference argument it made every access generic
@@ -99,9 +104,8 @@ __device__ __forceinline__ uint4* held_pieces() {
   return reinterpret_cast<uint4*>(sample_smem + sizeof(Shared));
 }
 
-__device__ __forceinline__ u64* keys() { return reinterpret_cast<u64*>(&shared().hist); }
+__device__ __forceinline__ u64* keys() { return shared().list; }
 __device__ __forceinline__ uint32_t* weights() {
-  Shared& sh = shared();
   return reinterpret_cast<uint32_t*>(keys() + kList);
 }
 
@@ -260,7 +264,7 @@ template <typename T, Mode MODE> struct Pieces {
   }
   // f(values, index of the first) for them
   template <typename F> __device__ __forceinline__ void each(int q0, int q1, F f) const {
-    each_piece<HELD ? 1 : 3>(q0, q1, [&](const uint4& r, int q, int) {
+    each_piece<HELD ? 1 : 2>(q0, q1, [&](const uint4& r, int q, int) {
       float v[V];
       values(r, v);
       f(v, q * V - mis);
@@ -372,18 +376,14 @@ __device__ __forceinline__ int pow2_at_least(int v) {
   return p;
 }
 
-// A block's own list; a block alone fills the joined one.
-__device__ __forceinline__ u64* own_list(const Team& team) {
-  Shared& sh = shared();
-  return team.size > 1 ? sh.list : keys();
-}
 __device__ __forceinline__ void append(const Team& team, u64 key) {
   Shared& sh = shared();
   const uint32_t at = atomicAdd(&sh.listed, 1u);
-  if (at < (uint32_t)(team.size > 1 ? kLocal : kList)) own_list(team)[at] = key;
+  // (a block alone goes on into the joined list)
+  if (at < (uint32_t)(team.size > 1 ? kLocal : kOpen)) keys()[at] = key;
 }
 
-// Tokens listed by all blocks of the cluster; more than kList when they do not
+// Tokens listed by all blocks of the cluster; more than kOpen when they do not
 // fit.  After a sync that follows the gathering; the caller syncs before the
 // lists are used again.
 __device__ __forceinline__ u64 listed_by_all(const Team& team) {
@@ -391,17 +391,18 @@ __device__ __forceinline__ u64 listed_by_all(const Team& team) {
   if (team.size == 1) return sh.listed;
   u64 total = 0;
   team.over(&sh.listed, [&](uint32_t c, int) {
-    total += c <= (uint32_t)kLocal ? (u64)c : (u64)kList + 1ull;
+    total += c <= (uint32_t)kLocal ? (u64)c : (u64)kOpen + 1ull;
   });
   return total;
 }
 
-// The first block's joined list gets all blocks' lists (they fit).
+// The first block's joined list gets the other blocks' lists behind its own
+// (they fit).
 __device__ void join_lists(const Team& team) {
   Shared& sh = shared();
   if (team.rank != 0 || team.size == 1) return;
   const int warp = threadIdx.x >> 5;                   // one warp a block's list
-  if (warp < team.size) {
+  if (warp > 0 && warp < team.size) {
     uint32_t at = 0, mine = 0;
     team.over(&sh.listed, [&](uint32_t c, int k) {
       if (k < warp) at += c;
@@ -739,15 +740,14 @@ __device__ __noinline__ u64 rank_open(const Team& team, const Row& r, const Sear
       const int per = (size + kThreads - 1) / kThreads;    // consecutive entries a thread
       const int p0 = threadIdx.x * per, p1 = min(p0 + per, len);
       u64 mine = 0;
-      for (int p = p0; p < p1; ++p) {
-        const uint32_t w = Row::weight(Row::e(r.depth(rank_logit(keys()[p]))));
-        weights()[p] = w;
-        mine += w;
-      }
+      auto weight_at = [&](int p) {
+        return Row::weight(Row::e(r.depth(rank_logit(keys()[p]))));
+      };
+      for (int p = p0; p < p1; ++p) mine += weight_at(p);
       u64 total;
       u64 mass = f.before_mass + block_scan(mine, &total);
       for (int p = p0; p < p1; ++p) {
-        const uint32_t w = weights()[p];
+        const uint32_t w = weight_at(p);
         const u64 lo = COUNT ? f.before_count + (u64)p : mass;
         const u64 hi = lo + (COUNT ? 1ull : (u64)w);
         if (lo < f.target && f.target <= hi) {
@@ -795,7 +795,7 @@ __device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, const Team& te
       });
       team.sync();
       const u64 open = listed_by_all(team);
-      if (open <= (u64)kList) return rank_open<COUNT>(team, r, f, (int)open, mass_out);
+      if (open <= (u64)kOpen) return rank_open<COUNT>(team, r, f, (int)open, mass_out);
     }
     started = false;
     team.sync();                       // counted by all before the next round clears
@@ -955,41 +955,46 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
   const float low = bin_low(r, f.bin);
   const int per = batches_per_stretch(q0, q1);
   sum_stretches(q0, q1, per, [&](int b0, int b1) {
-    u64 mine = 0;
+    uint32_t high_sum = 0, low_sum = 0, pieces = 0;  // of halves, as in draw_in_row()
     pc.each_above(b0, b1, low, [&](const float (&v)[V], int i0) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (!(v[j] >= low)) continue;
         const float x = r.depth(v[j]);
         const float e = Row::e(x);
-        const uint32_t w = Row::weight(e);
-        const int b = Row::bin(x);
-        if (b < f.bin) {
-          mine += e >= r.min_p ? w : 0u;           // above the open ones: kept
-        } else if (b == f.bin && w != 0u) {
+        const int b = (int)Row::bin_if_weight(x);    // (past the bins without a weight)
+        uint32_t h, l;                               // above the open ones: kept
+        Row::halves(b < f.bin && e >= r.min_p ? e : 0.f, &h, &l);
+        high_sum += h;
+        low_sum += l;
+        if (b == f.bin) {
           const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
-          if (key >= from) append(team, key);
+          if (key >= from && Row::weight(e) != 0u) append(team, key);
         }
       }
+      ++pieces;
     });
-    return mine;
+    const uint32_t ones = pieces * (uint32_t)V * Row::kOne;
+    return ((u64)(high_sum - ones) << 16) + (u64)(low_sum - ones);
   });
   team.sync();
   const u64 open = listed_by_all(team);
-  if (open > (u64)kList) {
+  if (open > (u64)kOpen) {
     const u64 cut = find_cut<false>(pc, q0, q1, team, r, top_p, f, true, &mass);
     draw_in_row<true, true>(a, row, pc, q0, q1, team, r, cut, u);
     return;
   }
   const u64 cut = rank_open<false>(team, r, f, (int)open, &mass);
-  // this block's open tokens that are kept join their stretches' sums
+  // this block's open tokens that are kept join their stretches' sums (the
+  // first block's list is the joined one now)
   const int parts = team.size * kWarps;
-  for (int i = threadIdx.x; i < (int)sh.listed; i += kThreads) {
-    const u64 key = own_list(team)[i];
+  const int mine = team.rank == 0 ? (int)open : (int)sh.listed;
+  for (int i = threadIdx.x; i < mine; i += kThreads) {
+    const u64 key = keys()[i];
     const float e = Row::e(r.depth(rank_logit(key)));
     if (key < cut || !(e >= r.min_p)) continue;
     const int q = ((int)rank_index(key) + pc.mis) / V;
     const int part = pc.part_of(q, parts);
+    if (part / kWarps != team.rank) continue;
     const int p0 = pc.first(part, parts), p1 = pc.first(part + 1, parts);
     const int seg = (q - p0) / (batches_per_stretch(p0, p1) * 32 * kShares);
     atomicAdd(&sh.seg[part - team.rank * kWarps][seg], (u64)Row::weight(e));
