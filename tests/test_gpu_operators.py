@@ -99,6 +99,27 @@ def test_norm_mx(fmt, m, k, dt):
     assert np.all((got == 0) | (np.sign(got) == np.sign(want)))
 
 
+@pytest.mark.parametrize("fmt", [wql.NORM_SAME, wql.NORM_E4M3])
+@pytest.mark.parametrize("shift", [1, 3, 8])
+def test_norm_any_alignment(fmt, shift):
+    """Tensors that start anywhere give what aligned ones give, and rows that
+    share 16 bytes leave each other alone."""
+    m, k = 5, 1003
+    x, r, w = norm_inputs(m, k, "bf16", 9)
+    want = wql.wql_add_rmsnorm(x.to(DEV), w.to(DEV), r.to(DEV), fmt=fmt)
+    off = [torch.empty(t.numel() + shift, dtype=t.dtype, device=DEV)[shift:].view(t.shape)
+           for t in (x, r, w)]
+    for o, t in zip(off, (x, r, w)):
+        o.copy_(t)
+    got = wql.wql_add_rmsnorm(off[0], off[2], off[1], fmt=fmt)
+    for a, b in zip(want, got):
+        if a is not None and fmt == wql.NORM_SAME:
+            # the order of the sum differs: one ulp of the output at most
+            assert np.all(np.abs(f64(a) - f64(b)) <= 2.0 ** -7 * np.abs(f64(a)))
+        elif a is not None:
+            assert np.all(np.abs(f64(a.float()) - f64(b.float())) <= 2.0 ** -3 * np.abs(f64(a.float())) + 2.0 ** -9)
+
+
 def test_norm_in_place_and_leading_shape():
     x, r, w = norm_inputs(6, 512, "bf16", 1)
     xd, rd, wd = x.view(2, 3, 512).to(DEV), r.view(2, 3, 512).to(DEV), w.to(DEV)

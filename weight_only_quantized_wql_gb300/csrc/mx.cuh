@@ -48,48 +48,52 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
 // Eight values, already divided by the scale, to codes: 4 bytes (FP4, element
 // 0 in the lowest nibble) or 8 (FP8); round to nearest even, saturating.
 __device__ __forceinline__ uint32_t mx_codes_fp4(const float (&v)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b =
-        __nv_cvt_float2_to_fp4x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_E2M1, cudaRoundNearest);
-    w |= (b & 0xFFu) << (8 * i);
-  }
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+__device__ __forceinline__ uint32_t mx_codes_fp8x4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return w;
 }
 __device__ __forceinline__ uint2 mx_codes_fp8(const float (&v)[8]) {
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h], v[4 * h + 1]),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2], v[4 * h + 3]),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    w[h] = (lo & 0xFFFFu) | (hi << 16);
-  }
-  return make_uint2(w[0], w[1]);
+  return make_uint2(mx_codes_fp8x4(v[0], v[1], v[2], v[3]), mx_codes_fp8x4(v[4], v[5], v[6], v[7]));
 }
 
-__device__ __forceinline__ void mx_values_fp4(uint32_t w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw h =
-        __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+// Codes to their values as fp16 pairs (exact), element 0 in the low half of h[0].
+__device__ __forceinline__ void mx_halves_fp4(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
-__device__ __forceinline__ void mx_values_fp8(uint2 w, float (&v)[8]) {
-  const uint32_t p[2] = {w.x, w.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)((p[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ void mx_halves_fp8(uint2 w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "mov.b32 {a, b}, %4;\n\t"
+      "mov.b32 {c, d}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w.x), "r"(w.y));
 }
 
 // max(|a|, |b|), NaN if either is.
@@ -100,15 +104,13 @@ __device__ __forceinline__ float mx_max_abs(float a, float b) {
 }
 
 // A group of four consecutive lanes holds a block, eight values each: encode
-// this lane's eight (`x` in fp32) and return the block's scale byte.
+// this lane's eight (`x` in fp32, whose largest |x| has the float bits `amax`)
+// and return the block's scale byte.
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint2* codes) {
-  const float m = mx_max_abs(mx_max_abs(mx_max_abs(x[0], x[1]), mx_max_abs(x[2], x[3])),
-                             mx_max_abs(mx_max_abs(x[4], x[5]), mx_max_abs(x[6], x[7])));
-  uint32_t am = __float_as_uint(m) & 0x7FFFFFFFu;
-  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-  const uint32_t byte = mx_scale_byte<FMT>(am);
+__device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint32_t amax, uint2* codes) {
+  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  const uint32_t byte = mx_scale_byte<FMT>(amax);
   const float inv = mx_inverse(byte);
   float v[8];
 #pragma unroll
@@ -120,6 +122,11 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint2* codes
     *codes = mx_codes_fp8(v);
   }
   return byte;
+}
+__device__ __forceinline__ uint32_t mx_amax8(const float (&x)[8]) {
+  const float m = mx_max_abs(mx_max_abs(mx_max_abs(x[0], x[1]), mx_max_abs(x[2], x[3])),
+                             mx_max_abs(mx_max_abs(x[4], x[5]), mx_max_abs(x[6], x[7])));
+  return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
 // Tensor map (host) of a row-major matrix of rows of row_bytes, seen as

@@ -12,6 +12,8 @@
 // tiles come from a multiplication by the reciprocal of the tile count, and
 // each block's first lane stores its scale byte: with divisions, and a word of
 // scales gathered by shuffles, 151936 x 1024 fp16 to e2m1 and back took 158 us.
+#include <type_traits>
+
 #include "mx.cuh"
 
 namespace wql {
@@ -21,19 +23,39 @@ constexpr int kThreads = 256;
 constexpr int kHalfWarps = kThreads / 16;
 constexpr int kUnroll = 4;
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = ldg_stream_u4(p);
-    const T* h = reinterpret_cast<const T*>(&a);
+// Eight consecutive elements as loaded, their values, and the float bits of the
+// largest magnitude (NaNs on top; 16-bit types two at a time).
+template <typename T> struct Eight {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = ldg_stream_u4(p); }
+  __device__ __forceinline__ void clear() { raw = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const T* h = reinterpret_cast<const T*>(&raw);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = to_f32(h[i]);
   }
-}
+  __device__ __forceinline__ uint32_t amax(const float (&)[8]) const {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                         __nv_bfloat162>::type;
+    const T2* h = reinterpret_cast<const T2*>(&raw);
+    const T2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                             __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    return __float_as_uint(to_f32(__hmax_nan(m.x, m.y))) & 0x7FFFFFFFu;
+  }
+};
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ uint32_t amax(const float (&v)[8]) const { return mx_amax8(v); }
+};
 
 // item / tile_cols, for items < 16 tile_cols + 64: exact with recip =
 // ceil(2^32 / tile_cols) while item * tile_cols < 2^32 (tile_cols <= 2^13)
@@ -59,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
   const T* x = reinterpret_cast<const T*>(a.x);
   // every half warp makes the same number of passes (the shuffles need whole warps)
   for (int i0 = 0; i0 < items; i0 += kUnroll * kHalfWarps) {
-    float v[kUnroll][8];
+    Eight<T> x8[kUnroll];
     int row[kUnroll], tc[kUnroll];
     bool in[kUnroll];
 #pragma unroll
@@ -70,15 +92,16 @@ __global__ void __launch_bounds__(kThreads)
       tc[u] = item - r * tile_cols;
       const int col = tc[u] * 128 + lane * 8;
       in[u] = item < items && row[u] < a.rows && col < a.k;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-      if (in[u]) load8(x + (size_t)row[u] * a.k + col, v[u]);
+      x8[u].clear();
+      if (in[u]) x8[u].load(x + (size_t)row[u] * a.k + col);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int item = i0 + u * kHalfWarps + hw;
       uint2 q;
-      const uint32_t byte = mx_encode8<FMT>(v[u], &q);
+      float v[8];
+      x8[u].values(v);
+      const uint32_t byte = mx_encode8<FMT>(v, x8[u].amax(v), &q);
       if (in[u]) {
         const size_t vec = ((size_t)row[u] * a.k + tc[u] * 128 + lane * 8) / 8;
         if constexpr (FMT == WQL_MX_FP4)
@@ -131,21 +154,41 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (!in[u]) continue;
-      const float s = mx_scale_value((sw[u] >> (8 * (lane >> 2))) & 0xFFu);
-      float v[8];
+      const uint32_t byte = (sw[u] >> (8 * (lane >> 2))) & 0xFFu;
+      uint32_t h[4];
       if constexpr (FMT == WQL_MX_FP4)
-        mx_values_fp4(q[u].x, v);
+        mx_halves_fp4(q[u].x, h);
       else
-        mx_values_fp8(q[u], v);
+        mx_halves_fp8(q[u], h);
       T* dst = reinterpret_cast<T*>(a.out) + (size_t)row[u] * a.k + col[u];
+      if constexpr (std::is_same<T, __half>::value) {
+        // 2^-24 .. 2^15 are fp16 numbers: the product rounds once, as from fp32
+        if (byte >= 103u && byte <= 142u) {
+          const __half2 s = __half2half2(__float2half_rn(mx_scale_value(byte)));
+          uint4 o;
+          __half2* o2 = reinterpret_cast<__half2*>(&o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o2[j] = __hmul2(*reinterpret_cast<const __half2*>(&h[j]), s);
+          *reinterpret_cast<uint4*>(dst) = o;
+          continue;
+        }
+      }
+      const float s = mx_scale_value(byte);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        v[2 * j] = f.x * s;
+        v[2 * j + 1] = f.y * s;
+      }
       if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
       } else {
         uint4 o;
-        T* h = reinterpret_cast<T*>(&o);
+        T* t = reinterpret_cast<T*>(&o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = from_f32<T>(v[j] * s);
+        for (int j = 0; j < 8; ++j) t[j] = from_f32<T>(v[j]);
         *reinterpret_cast<uint4*>(dst) = o;
       }
     }

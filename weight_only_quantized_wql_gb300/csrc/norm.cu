@@ -12,6 +12,7 @@ namespace wql {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kMaxRagged = 65536 - 16;   // its groups may be two more than k / 8
 
 // Sum or maximum over the block; every thread gets it.
 template <bool MAX>
@@ -78,9 +79,12 @@ __device__ __forceinline__ void pad_scales(const NormArgs& a, int64_t row) {
 }
 
 // A thread holds G groups of W elements: group g of the row is thread
-// g % threads, slot g / threads.  W = 8 needs k % 8 == 0 and 16-byte aligned
-// tensors; W = 1 takes any width and alignment.
-template <typename T, int OUT, int W, int G>
+// g % threads, slot g / threads.  W = 8: 16-byte accesses, for 16-byte aligned
+// tensors; without RAGGED k % 8 == 0, with it groups start on 16-byte
+// addresses, `mis` elements before the row's first one, and those at the ends
+// (which share their 16 bytes with other rows) go element by element.  W = 1
+// takes any alignment.  (2000 x 4099 fp16 took 34.9 us by elements.)
+template <typename T, int OUT, int W, int G, bool RAGGED>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float red[32];
   griddep_launch_dependents();
@@ -92,10 +96,32 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
       return;
     }
   }
-  const int groups = a.k / W;
-  const T* x = reinterpret_cast<const T*>(a.x) + row * a.k;
-  const T* res = a.residual ? reinterpret_cast<const T*>(a.residual) + row * a.k : nullptr;
-  const T* gamma = reinterpret_cast<const T*>(a.gamma);
+  const int mis = RAGGED ? (int)((row * a.k) & 7) : 0;
+  const int groups = RAGGED ? (a.k + mis + 7) / 8 : a.k / W;
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.k - mis;
+  const T* res = a.residual ? reinterpret_cast<const T*>(a.residual) + row * a.k - mis : nullptr;
+  const T* gamma = reinterpret_cast<const T*>(a.gamma) - mis;
+  // is group g all inside the row; is its element i
+  auto whole = [&](int g) { return !RAGGED || (g * 8 >= mis && g * 8 + 8 <= a.k + mis); };
+  auto inside = [&](int g, int i) { return g * 8 + i >= mis && g * 8 + i < a.k + mis; };
+  auto load = [&](const T* p, int g, float (&v)[W]) {
+    if (whole(g)) {
+      load_group<T, W>(p + (size_t)g * W, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = inside(g, i) ? to_f32(p[(size_t)g * W + i]) : 0.f;
+    }
+  };
+  auto store = [&](void* out, int g, const float (&v)[W]) {
+    T* p = reinterpret_cast<T*>(out) + row * a.k - mis + (size_t)g * W;
+    if (whole(g)) {
+      store_group<T, W>(p, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (inside(g, i)) p[i] = from_f32<T>(v[i]);
+    }
+  };
   float h[G][W];
   float sum = 0.f;
 #pragma unroll
@@ -103,7 +129,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
     const int g = j * blockDim.x + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < W; ++i) h[j][i] = 0.f;
-    if (g < groups) load_group<T, W>(x + (size_t)g * W, h[j]);
+    if (g < groups) load(x, g, h[j]);
   }
   if (res) {
 #pragma unroll
@@ -111,7 +137,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
       const int g = j * blockDim.x + threadIdx.x;
       float r[W];
       if (g < groups) {
-        load_group<T, W>(res + (size_t)g * W, r);
+        load(res, g, r);
 #pragma unroll
         for (int i = 0; i < W; ++i) h[j][i] += r[i];
       }
@@ -131,10 +157,14 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
   for (int j = 0; j < G; ++j) {
     const int g = j * blockDim.x + threadIdx.x;
     if (g < groups) {
-      if (a.residual_out)
-        store_group<T, W>(reinterpret_cast<T*>(a.residual_out) + row * a.k + (size_t)g * W, h[j]);
+      if (a.residual_out) store(a.residual_out, g, h[j]);
       float gm[W];
-      load_group<T, W>(gamma + (size_t)g * W, gm);
+      if constexpr (RAGGED) {             // gamma starts on its own boundary: by elements
+#pragma unroll
+        for (int i = 0; i < W; ++i) gm[i] = inside(g, i) ? to_f32(gamma[g * W + i]) : 0.f;
+      } else {
+        load_group<T, W>(gamma + (size_t)g * W, gm);
+      }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         h[j][i] = h[j][i] * scale * gm[i];
@@ -147,8 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int g = j * blockDim.x + threadIdx.x;
-      if (g < groups)
-        store_group<T, W>(reinterpret_cast<T*>(a.out) + row * a.k + (size_t)g * W, h[j]);
+      if (g < groups) store(a.out, g, h[j]);
     }
   } else if constexpr (OUT == WQL_NORM_E4M3) {
     amax = block_reduce<true>(amax, red);
@@ -156,7 +185,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
     const float s = s0 < 1e-8f ? 1e-8f : s0;          // (a NaN stays)
     const float inv = __fdiv_rn(1.f, s);
     if (threadIdx.x == 0) reinterpret_cast<float*>(a.scales)[row] = s;
-    uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.k;
+    uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.k - mis;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int g = j * blockDim.x + threadIdx.x;
@@ -165,7 +194,15 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = h[j][i] * inv;
-        *reinterpret_cast<uint2*>(out + (size_t)g * 8) = mx_codes_fp8(v);
+        const uint2 q = mx_codes_fp8(v);
+        if (whole(g)) {
+          *reinterpret_cast<uint2*>(out + (size_t)g * 8) = q;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (inside(g, i))
+              out[(size_t)g * 8 + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+        }
       } else {
         out[g] = (uint8_t)__nv_cvt_float_to_fp8(h[j][0] * inv, __NV_SATFINITE, __NV_E4M3);
       }
@@ -181,7 +218,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
       // zeros with scale 0
       const int g = j * blockDim.x + threadIdx.x;
       uint2 q;
-      const uint32_t byte = mx_encode8<FMT>(h[j], &q);
+      const uint32_t byte = mx_encode8<FMT>(h[j], mx_amax8(h[j]), &q);
       if (g < groups) {
         const size_t vec = (size_t)row * groups + g;
         if constexpr (FMT == WQL_MX_FP4)
@@ -196,43 +233,43 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const NormArgs
   }
 }
 
-template <typename T, int OUT, int W, int G>
+template <typename T, int OUT, int W, int G, bool RAGGED>
 cudaError_t launch_g(const NormArgs& a, int threads, cudaStream_t s) {
   const int rows = OUT >= WQL_NORM_MX_FP8
                        ? (a.m + kMxTileRows - 1) / kMxTileRows * kMxTileRows : a.m;
   const cudaError_t e =
-      launch_pdl(add_rmsnorm_kernel<T, OUT, W, G>, dim3((unsigned)rows), dim3(threads), 0, s, a);
+      launch_pdl(add_rmsnorm_kernel<T, OUT, W, G, RAGGED>, dim3((unsigned)rows), dim3(threads), 0, s, a);
   note_launch();
   return e;
 }
 
-template <typename T, int OUT, int W>
+template <typename T, int OUT, int W, bool RAGGED = false>
 cudaError_t launch_w(const NormArgs& a, cudaStream_t s) {
   // Threads per row: few rows want all their loads out at once (1 x 5120: 640
-  // threads, one group each), many rows small blocks with several loads per
-  // thread; single elements always more threads.
-  const int groups = a.k / W;
-  const int most = a.m < 2 * device_sm_count() ? kMaxThreads : W == 1 ? 512 : 256;
+  // threads, one group each), many rows several loads per thread (4096 x 5120
+  // to e4m3: 25.9 us with at most 512 threads, 29.2 with 256, 29.0 with 1024).
+  const int groups = RAGGED ? a.k / W + 2 : a.k / W;
+  const int most = a.m < 2 * device_sm_count() ? kMaxThreads : 512;
   int g = 1;
   while (g < 64 / W && groups > most * g) g *= 2;
   int threads = ((groups + g - 1) / g + 31) / 32 * 32;
   if (threads > kMaxThreads) return cudaErrorInvalidConfiguration;
   if constexpr (W == 8) {
     switch (g) {
-      case 1: return launch_g<T, OUT, W, 1>(a, threads, s);
-      case 2: return launch_g<T, OUT, W, 2>(a, threads, s);
-      case 4: return launch_g<T, OUT, W, 4>(a, threads, s);
-      default: return launch_g<T, OUT, W, 8>(a, threads, s);
+      case 1: return launch_g<T, OUT, W, 1, RAGGED>(a, threads, s);
+      case 2: return launch_g<T, OUT, W, 2, RAGGED>(a, threads, s);
+      case 4: return launch_g<T, OUT, W, 4, RAGGED>(a, threads, s);
+      default: return launch_g<T, OUT, W, 8, RAGGED>(a, threads, s);
     }
   } else {
     switch (g) {
-      case 1: return launch_g<T, OUT, W, 1>(a, threads, s);
-      case 2: return launch_g<T, OUT, W, 2>(a, threads, s);
-      case 4: return launch_g<T, OUT, W, 4>(a, threads, s);
-      case 8: return launch_g<T, OUT, W, 8>(a, threads, s);
-      case 16: return launch_g<T, OUT, W, 16>(a, threads, s);
-      case 32: return launch_g<T, OUT, W, 32>(a, threads, s);
-      default: return launch_g<T, OUT, W, 64>(a, threads, s);
+      case 1: return launch_g<T, OUT, W, 1, RAGGED>(a, threads, s);
+      case 2: return launch_g<T, OUT, W, 2, RAGGED>(a, threads, s);
+      case 4: return launch_g<T, OUT, W, 4, RAGGED>(a, threads, s);
+      case 8: return launch_g<T, OUT, W, 8, RAGGED>(a, threads, s);
+      case 16: return launch_g<T, OUT, W, 16, RAGGED>(a, threads, s);
+      case 32: return launch_g<T, OUT, W, 32, RAGGED>(a, threads, s);
+      default: return launch_g<T, OUT, W, 64, RAGGED>(a, threads, s);
     }
   }
 }
@@ -240,13 +277,17 @@ cudaError_t launch_w(const NormArgs& a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_t(const NormArgs& a, cudaStream_t s) {
   auto ok = [](const void* p, size_t al) { return (reinterpret_cast<uintptr_t>(p) % al) == 0; };
-  const bool wide = a.k % 8 == 0 && ok(a.x, 16) && ok(a.residual, 16) && ok(a.gamma, 16) &&
-                    ok(a.residual_out, 16) && ok(a.out, a.out_format == WQL_NORM_E4M3 ? 8 : 16);
+  const bool wide = ok(a.x, 16) && ok(a.residual, 16) && ok(a.residual_out, 16) &&
+                    ok(a.out, a.out_format == WQL_NORM_E4M3 ? 8 : 16);
+  const bool even = wide && a.k % 8 == 0 && ok(a.gamma, 16);
+  const bool ragged = wide && a.k <= kMaxRagged;
   switch (a.out_format) {
     case WQL_NORM_SAME:
-      return wide ? launch_w<T, WQL_NORM_SAME, 8>(a, s) : launch_w<T, WQL_NORM_SAME, 1>(a, s);
+      return even ? launch_w<T, WQL_NORM_SAME, 8>(a, s)
+             : ragged ? launch_w<T, WQL_NORM_SAME, 8, true>(a, s) : launch_w<T, WQL_NORM_SAME, 1>(a, s);
     case WQL_NORM_E4M3:
-      return wide ? launch_w<T, WQL_NORM_E4M3, 8>(a, s) : launch_w<T, WQL_NORM_E4M3, 1>(a, s);
+      return even ? launch_w<T, WQL_NORM_E4M3, 8>(a, s)
+             : ragged ? launch_w<T, WQL_NORM_E4M3, 8, true>(a, s) : launch_w<T, WQL_NORM_E4M3, 1>(a, s);
     case WQL_NORM_MX_FP8: return launch_w<T, WQL_NORM_MX_FP8, 8>(a, s);
     default: return launch_w<T, WQL_NORM_MX_FP4, 8>(a, s);
   }
