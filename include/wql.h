@@ -343,7 +343,8 @@ wql_status wql_mx_dequantize(const wql_mx* a, int32_t out_dtype, void* out,
  *   workspace  device, 256-byte aligned, zero-filled once, ws_bytes >=
  *              wql_workspace_size(m, n, 0), or NULL.  A bounded wait of the
  *              kernel that runs out records bit 8 in its error word (bytes
- *              4..7, sticky); with NULL it is not recorded.
+ *              4..7, sticky), and the logits are not valid; with NULL it is
+ *              not recorded.
  * A NaN scale (or an fp8 NaN code) gives NaN logits for its row or column. */
 wql_status wql_mx_logits(const wql_mx* x, const wql_mx* w, const void* bias,
                          int32_t out_dtype, void* logits_out, void* workspace,
@@ -414,15 +415,15 @@ wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n,
 const char* wql_status_string(wql_status status);
 
 /* Diagnostics, for tests of the timeout path.  Every wait inside the kernels
- * is bounded; a wait that runs out records bit 2 (tensor-core kernel) or 4
- * (top-K selection) in the workspace's error word (bytes 4..7, sticky until
+ * is bounded; a wait that runs out records bit 2 (tensor-core kernel), 4
+ * (top-K selection) or 8 (wql_mx_logits) in the workspace's error word (bytes 4..7, sticky until
  * the caller zeroes it), the kernel finishes without leaving copies or
  * tensor-core work in flight, and from then on the top-K outputs of every
  * call on that workspace read index -1 and value NaN.
- *   budget_cycles  SM cycles a wait of the tensor-core kernel on a ring slot
+ *   budget_cycles  SM cycles a wait of the tensor-core kernels on a ring slot
  *                  or on data may take (0: the default, about 1 s); the
  *                  waits for a CTA's own copies keep the default
- *   stall_mma      1: the tensor-core kernel's MMA warp first waits on a
+ *   stall_mma      1: the tensor-core kernels' MMA warp first waits on a
  *                  barrier nothing arrives on, so that its budget runs out
  *                  and every other role's waits run out after it
  * Process-wide, for the calls launched after it; not for concurrent use.

@@ -284,6 +284,25 @@ def test_mx_logits_extreme_scales():
     check_logits(wql.wql_mx_logits(xa, wa, torch.bfloat16), xv, wv, "bf16")
 
 
+@pytest.mark.parametrize("fmt,k", [(wql.MX_FP8, 512), (wql.MX_FP8, 544), (wql.MX_FP4, 512)])
+def test_mx_logits_wait_timeout_is_reported_and_recovers(fmt, k):
+    """A stalled issuing warp: every role's bounded wait runs out, the call
+    returns, the error word says so, and the next call is right."""
+    xa, wa, xv, wv = mx_operands(20, 3000, k, fmt, 1)
+    ws = wql.Workspace(DEV)
+    try:
+        wql.wql_debug_set_waits(2_000_000, True)          # SM cycles, about 1 ms
+        wql.wql_mx_logits(xa, wa, torch.float16, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        wql.wql_debug_set_waits(0, False)
+    assert ws.error_word() == 8
+    ws.clear_error()
+    got = wql.wql_mx_logits(xa, wa, torch.float16, workspace=ws)
+    assert ws.error_word() == 0
+    check_logits(got, xv, wv, "f16")
+
+
 # ---------------------------------------------------------------------------
 # sampling
 # ---------------------------------------------------------------------------
@@ -477,3 +496,19 @@ def test_step_on_a_side_stream():
     side.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def test_example_decodes_the_same_eagerly_and_as_a_graph():
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "decode_step", os.path.join(root, "examples", "decode_step.py"))
+    ex = importlib.util.module_from_spec(spec)
+    import sys
+    sys.modules["decode_step"] = ex
+    spec.loader.exec_module(ex)
+    eager, logp = ex.decode(3, 4099, 256, 5, graph=False)
+    graph, logp2 = ex.decode(3, 4099, 256, 5, graph=True)
+    assert torch.equal(eager, graph) and torch.equal(logp, logp2)
+    assert eager.min() >= 0 and eager.max() < 4099 and (logp <= 0).all()

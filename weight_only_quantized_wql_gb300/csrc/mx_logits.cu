@@ -91,6 +91,8 @@ struct MxParams {
   uint32_t off_out;                // staging of the stores
   int out_bufs;                    // buffers of each epilogue group
   long long wait_budget;
+  int diag_stall;                  // diagnostics: the issuing warp first waits on a barrier
+                                   // nothing arrives on (the timeout path runs)
 };
 
 // 3-D tiled TMA load of one box.
@@ -223,7 +225,8 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* x_full = acc_empty + 2;
   uint64_t* drain = x_full + kMaxResident;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* stall = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stall + 1);
   unsigned int* failed = tmem_slot + 1;
 
   const MxLogitsArgs& a = p.a;
@@ -247,6 +250,7 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
     }
     for (int c = 0; c < kMaxResident; ++c) mbar_init(&x_full[c], 1);
     mbar_init(drain, 1);
+    mbar_init(stall, 1);
     *failed = 0u;
     fence_barrier_init();
   }
@@ -362,6 +366,7 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
     int slot = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0, set = 0;
     bool issued = false;
+    if (p.diag_stall) bad = !mbar_wait(stall, 0u, p.wait_budget);
     for (int t = t0; t < t1; ++t) {
       if (!bad && t - t0 >= p.acc_bufs) bad = !mbar_wait(&acc_empty[acc], acc_phase ^ 1u, p.wait_budget);
       if (__any_sync(0xFFFFFFFFu, bad)) { bad = true; break; }
@@ -494,42 +499,45 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
                                      (((piece & 7) ^ (r0 & 7)) * 16));
     const size_t pitch = (size_t)a.k / 2;
     const uint8_t* w = reinterpret_cast<const uint8_t*>(a.w_codes);
-    int slot = 0, done_slot = 0;
+    int slot = 0, handed_slot = 0, issued = 0, handed = 0;
     uint32_t phase = 0;
+    auto hand_on = [&] {
+      // the tensor core reads through the async proxy
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[handed_slot]);
+      if (++handed_slot == p.ring) handed_slot = 0;
+      ++handed;
+    };
     int t = t0, c = 0;
-    for (int i = 0; i < steps + p.copy_depth; ++i) {
-      if (i < steps) {
-        if (i >= p.ring) bad = bad || !mbar_wait(&empty[slot], phase ^ 1u, p.wait_budget);
-        bad = __any_sync(0xFFFFFFFFu, bad);
-        if (bad) break;
-        const int col = c * kCols + piece * 16;
-        if (col < a.k) {
-          const uint32_t dst = base + (uint32_t)slot * p.stage_bytes + unit;
-          const uint8_t* src = w + col / 2;
+    for (; issued < steps; ++issued) {
+      if (issued >= p.ring) bad = !mbar_wait(&empty[slot], phase ^ 1u, p.wait_budget);
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (bad) break;
+      const int col = c * kCols + piece * 16;
+      if (col < a.k) {
+        const uint32_t dst = base + (uint32_t)slot * p.stage_bytes + unit;
+        const uint8_t* src = w + col / 2;
 #pragma unroll
-          for (int r = 0; r < kTileRows; r += 8)
-            // rows past the last repeat it; their logits are not stored
-            cp_async8(dst + r * 128, src + (size_t)min(t * kTileRows + r0 + r, a.n - 1) * pitch);
-        }
-        if (++slot == p.ring) { slot = 0; phase ^= 1u; }
-        if (++c == p.stages_k) { c = 0; ++t; }
+        for (int r = 0; r < kTileRows; r += 8)
+          // rows past the last repeat it; their logits are not stored
+          cp_async8(dst + r * 128, src + (size_t)min(t * kTileRows + r0 + r, a.n - 1) * pitch);
       }
       cp_async_commit();
-      if (i >= p.copy_depth) {
+      if (++slot == p.ring) { slot = 0; phase ^= 1u; }
+      if (++c == p.stages_k) { c = 0; ++t; }
+      if (issued >= p.copy_depth) {
         if (p.copy_depth == 3)
           cp_async_wait<3>();
         else if (p.copy_depth == 2)
           cp_async_wait<2>();
         else
           cp_async_wait<1>();
-        // the tensor core reads through the async proxy
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[done_slot]);
-        if (++done_slot == p.ring) done_slot = 0;
+        hand_on();
       }
     }
     cp_async_wait<0>();
+    while (handed < issued) hand_on();
   }
 
   if (bad) atomicOr(failed, 1u);
@@ -593,6 +601,7 @@ cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
   MxParams p{};
   p.a = a;
   p.wait_budget = diag_wait_budget();
+  p.diag_stall = diag_stall_mma();
   p.tiles = (a.n + kTileRows - 1) / kTileRows;
   p.tile_cols = (int)mx_tile_cols(a.k);
   p.stages_k = (a.k + kCols - 1) / kCols;
