@@ -244,36 +244,53 @@ template <typename T, Mode MODE> struct Pieces {
       r[u] = q < q1 ? load(q) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  // f(piece, its number, turn) for this warp's pieces q0 .. q1: one a turn, the
-  // loads of the next D - 1 in flight; turn = 0 .. D-1
+  // f(piece, its number, u) for this warp's pieces q0 .. q1, D a turn without a
+  // check (u = 0 .. D-1), then the rest
   template <int D, typename F>
   __device__ __forceinline__ void each_piece(int q0, int q1, F f) const {
-    int q = q0 + (int)(threadIdx.x & 31);
-    uint4 r[D];
-#pragma unroll
-    for (int u = 0; u < D; ++u)
-      if (q + u * 32 < q1) r[u] = load(q + u * 32);
+    const int lane = threadIdx.x & 31;
+    int q = q0;
+    if constexpr (MODE == kRagged && D > 1) {
+      if (q == 0) {                    // with the row's first piece: by themselves
 #pragma unroll 1
-    for (; q < q1; q += 32 * D) {
-#pragma unroll
-      for (int u = 0; u < D; ++u) {
-        if (q + u * 32 < q1) f(r[u], q + u * 32, u);
-        if (q + (u + D) * 32 < q1) r[u] = load(q + (u + D) * 32);
+        for (const int q2 = min(q1, 32 * D); q < q2; q += 32)
+          if (q + lane < q2) f(load(q + lane), q + lane, 0);
+        q = min(q1, 32 * D);
       }
     }
+    const int whole = MODE == kRagged && q1 == pieces ? q1 - 1 : q1;
+    if constexpr (D > 1) {
+#pragma unroll 1
+      for (; q + 32 * D <= whole; q += 32 * D) {
+        uint4 r[D];
+        if constexpr (HELD) {
+          const uint4* p = held_pieces() + (q + lane - s0);
+#pragma unroll
+          for (int u = 0; u < D; ++u) r[u] = p[u * 32];
+        } else {
+          const uint4* p = reinterpret_cast<const uint4*>(base) + (q + lane);
+#pragma unroll
+          for (int u = 0; u < D; ++u) r[u] = __ldg(p + u * 32);
+        }
+#pragma unroll
+        for (int u = 0; u < D; ++u) f(r[u], q + u * 32 + lane, u);
+      }
+    }
+#pragma unroll 1
+    for (q += lane; q < q1; q += 32) f(load(q), q, 0);
   }
   // f(values, index of the first) for them
   template <typename F> __device__ __forceinline__ void each(int q0, int q1, F f) const {
-    each_piece<HELD ? 1 : 2>(q0, q1, [&](const uint4& r, int q, int) {
+    each_piece<HELD ? 1 : 16 / V>(q0, q1, [&](const uint4& r, int q, int) {
       float v[V];
       values(r, v);
       f(v, q * V - mis);
     });
   }
-  // and for those whose largest value reaches `low`
-  template <typename F>
+  // and for those whose largest value reaches `low`, D a turn
+  template <int D, typename F>
   __device__ __forceinline__ void each_above(int q0, int q1, float low, F f) const {
-    each_piece<HELD ? 1 : 3>(q0, q1, [&](const uint4& r, int q, int) {
+    each_piece<HELD ? 1 : D>(q0, q1, [&](const uint4& r, int q, int) {
       if (max_of(r) >= low) {
         float v[V];
         values(r, v);
@@ -597,24 +614,25 @@ struct Search {
   int bin = -1;        // chosen quarter octave
   u64 prefix = 0;      // chosen leading digits of the rank key
   int shift = 8 * 7;   // bits of the rank key (32 + 20) still open
+  bool clean = false;  // the histograms are as the kernel's start left them
 };
 
 // One round: a histogram of the open tokens, by quarter octave first and then
 // by the next seven bits of the rank key, and in it the digit at which the
 // running count (COUNT) or weight reaches the target.  For a nucleus the
 // target follows from the first histogram, whose total is the sum of all
-// weights.  False when the total stays below the target; *total_mass gets it.
+// weights.  False when the total stays below the target.
 template <bool COUNT, typename P>
 __device__ __noinline__ bool search_round(const P& pc, int q0, int q1,
-                                          const Team& team, const Row& r, float top_p, Search& f,
-                                          u64* total_mass) {
+                                          const Team& team, const Row& r, float top_p, Search& f) {
   Shared& sh = shared();
   constexpr int V = P::V;
   constexpr int kDigitBits = 7;
   const int copy = threadIdx.x & (kCopies - 1);
   const bool first = f.bin < 0;
   const int dshift = first ? f.shift : f.shift - kDigitBits;
-  clear_hist();
+  if (!f.clean) clear_hist();
+  f.clean = false;
   if (threadIdx.x == 0) {
     sh.digit = -1;
     sh.listed = 0u;
@@ -671,7 +689,6 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1,
   u64 total, total_count;
   const u64 to_mass = f.before_mass + block_scan(mass, &total);
   const u64 to_count = COUNT ? f.before_count + block_scan(cnt, &total_count) : 0ull;
-  *total_mass = total;
   if (!COUNT && first) f.target = nucleus_target(top_p, total);
   const u64 lo = COUNT ? to_count : to_mass, hi = lo + (COUNT ? cnt : mass);
   if (lo < f.target && f.target <= hi) {
@@ -703,11 +720,10 @@ __device__ __forceinline__ float bin_high(const Row& r, int bin) {
 }
 
 // The open tokens, joined and ranked by the first block: the rank key of the
-// one at which the target is reached, and (*mass) the weights up to it.
-// Ends with a sync.
+// one at which the target is reached.
 template <bool COUNT>
 __device__ __noinline__ u64 rank_open(const Team& team, const Row& r, const Search& f,
-                                      int len, u64* mass_out) {
+                                      int len) {
   Shared& sh = shared();
   join_lists(team);
   if (team.rank == 0) {
@@ -731,7 +747,6 @@ __device__ __noinline__ u64 rank_open(const Team& team, const Row& r, const Sear
       const u64 hi = lo + (COUNT ? 1ull : (u64)w);
       if (p < len && part == 0 && lo < f.target && f.target <= hi) {
         sh.cut = key;
-        sh.sum = mass + w;
       }
     } else {
       const int size = pow2_at_least(len);
@@ -752,37 +767,31 @@ __device__ __noinline__ u64 rank_open(const Team& team, const Row& r, const Sear
         const u64 hi = lo + (COUNT ? 1ull : (u64)w);
         if (lo < f.target && f.target <= hi) {
           sh.cut = keys()[p];
-          sh.sum = mass + w;
         }
         mass += w;
       }
     }
   }
   team.sync();
-  const u64 cut = *team.of(&sh.cut, 0);
-  *mass_out = *team.of(&sh.sum, 0);
-  team.sync();
-  return cut;
+  return *team.of(&sh.cut, 0);         // (written again only after further syncs)
 }
 
 // The rank key of the last token of the shortest prefix that reaches the
-// search's target; 0 when all tokens together do not.  *mass_out gets the
-// prefix's sum of weights.  `f` may have its first round behind it (`started`).
+// search's target; 0 when all tokens together do not.  `f` may have its first round behind it (`started`).
 template <bool COUNT, typename P>
 __device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, const Team& team,
-                                     const Row& r, float top_p, Search& f, bool started,
-                                     u64* mass_out) {
+                                     const Row& r, float top_p, Search& f, bool started) {
   Shared& sh = shared();
   constexpr int V = P::V;
   for (;;) {
-    if (!started && !search_round<COUNT>(pc, q0, q1, team, r, top_p, f, mass_out)) {
+    if (!started && !search_round<COUNT>(pc, q0, q1, team, r, top_p, f)) {
       team.sync();
       return 0ull;
     }
     if (!started) {
       // gather the open tokens; the bounds are generous, the test is exact
       const float low = bin_low(r, f.bin), high = bin_high(r, f.bin);
-      pc.each_above(q0, q1, low, [&](const float (&v)[V], int i0) {
+      pc.template each_above<2>(q0, q1, low, [&](const float (&v)[V], int i0) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
           if (v[j] >= low && v[j] <= high) {
@@ -795,7 +804,7 @@ __device__ __noinline__ u64 find_cut(const P& pc, int q0, int q1, const Team& te
       });
       team.sync();
       const u64 open = listed_by_all(team);
-      if (open <= (u64)kOpen) return rank_open<COUNT>(team, r, f, (int)open, mass_out);
+      if (open <= (u64)kOpen) return rank_open<COUNT>(team, r, f, (int)open);
     }
     started = false;
     team.sync();                       // counted by all before the next round clears
@@ -905,7 +914,7 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
   sum_stretches(q0, q1, per, [&](int b0, int b1) {
     u64 mine = 0;
     if constexpr (CUT) {
-      pc.each_above(b0, b1, lowest, [&](const float (&v)[V], int i0) {
+      pc.template each_above<2>(b0, b1, lowest, [&](const float (&v)[V], int i0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           if (!(v[j] >= lowest) ||
@@ -944,19 +953,19 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
 template <typename P>
 __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P& pc, int q0,
                                           int q1, const Team& team, const Row& r,
-                                          u64 from, float top_p, float u) {
+                                          u64 from, float top_p, float u, bool clean) {
   Shared& sh = shared();
   constexpr int V = P::V;
   Search f;
   f.from = from;
-  u64 mass;
+  f.clean = clean;
   // (always found: the largest weight is 2^31)
-  search_round<false>(pc, q0, q1, team, r, top_p, f, &mass);
+  search_round<false>(pc, q0, q1, team, r, top_p, f);
   const float low = bin_low(r, f.bin);
   const int per = batches_per_stretch(q0, q1);
   sum_stretches(q0, q1, per, [&](int b0, int b1) {
     uint32_t high_sum = 0, low_sum = 0, pieces = 0;  // of halves, as in draw_in_row()
-    pc.each_above(b0, b1, low, [&](const float (&v)[V], int i0) {
+    pc.template each_above<2>(b0, b1, low, [&](const float (&v)[V], int i0) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float x = r.depth(v[j]);
@@ -979,11 +988,11 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
   team.sync();
   const u64 open = listed_by_all(team);
   if (open > (u64)kOpen) {
-    const u64 cut = find_cut<false>(pc, q0, q1, team, r, top_p, f, true, &mass);
+    const u64 cut = find_cut<false>(pc, q0, q1, team, r, top_p, f, true);
     draw_in_row<true, true>(a, row, pc, q0, q1, team, r, cut, u);
     return;
   }
-  const u64 cut = rank_open<false>(team, r, f, (int)open, &mass);
+  const u64 cut = rank_open<false>(team, r, f, (int)open);
   // this block's open tokens that are kept join their stretches' sums (the
   // first block's list is the joined one now)
   const int parts = team.size * kWarps;
@@ -1195,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // (a little below the edge, against the rounding here)
     const float bound = all ? __int_as_float(0xFF800000)
                             : r.top - ((float)sh.digit + 0.5f + 1e-3f) / (4.f * r.c);
-    pc.each_above(q0, q1, bound, [&](const float (&v)[V], int i0) {
+    pc.template each_above<4>(q0, q1, bound, [&](const float (&v)[V], int i0) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (v[j] >= bound && Row::weight(Row::e(r.depth(v[j]))) != 0u)
@@ -1222,11 +1231,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     Search f;
     f.from = 0ull;
     f.target = (u64)top_k;
-    u64 mass;
-    cut = find_cut<true>(pc, q0, q1, team, r, 1.f, f, false, &mass);
+    cut = find_cut<true>(pc, q0, q1, team, r, 1.f, f, false);
   }
   if (top_p < 1.f)
-    draw_nucleus(a, row, pc, q0, q1, team, r, cut, top_p, u);
+    draw_nucleus(a, row, pc, q0, q1, team, r, cut, top_p, u, top_k <= 0);
   else if (cut != 0ull)
     draw_in_row<true, true>(a, row, pc, q0, q1, team, r, cut, u);
   else if (r.min_p > 0.f)
