@@ -5,13 +5,13 @@
 // power of two is exact, so the only rounding is the code's.
 //
 // HBM-bound: quantising reads 2 (4) bytes an element and writes 17/32 (FP4)
-// or 33/32 (FP8).  A thread takes eight columns (one 16-byte load of 16-bit
-// input), four lanes a block, a half warp one scale tile's row (128 columns),
-// so the codes of a half warp are 64 or 128 consecutive bytes.  Loads of
-// several tiles are in flight per thread before the first is used; rows and
-// tiles come from a multiplication by the reciprocal of the tile count, and
-// each block's first lane stores its scale byte: with divisions, and a word of
-// scales gathered by shuffles, 151936 x 1024 fp16 to e2m1 and back took 158 us.
+// or 33/32 (FP8).  Quantising, a thread takes sixteen columns (two 16-byte
+// loads of 16-bit input), two lanes a block, eight lanes one scale tile's row
+// (128 columns); with eight columns a thread it was bound by instructions
+// (151936 x 1024 fp16 to e2m1 and back 128 us).  Dequantising, a thread takes
+// eight columns.  Loads of several tiles are in flight per thread before the
+// first is used; rows and tiles come from a multiplication by the reciprocal of
+// the tile count.
 #include <type_traits>
 
 #include "mx.cuh"
@@ -20,7 +20,10 @@ namespace wql {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHalfWarps = kThreads / 16;
+constexpr int kLanes = 8;                    // quantising: lanes per row of a scale tile
+constexpr int kTeams = kThreads / kLanes;
+constexpr int kTilesAhead = 2;               // per thread
+constexpr int kHalfWarps = kThreads / 16;    // dequantising: the lanes per row are 16
 constexpr int kUnroll = 4;
 
 // Eight consecutive elements as loaded, their values, and the float bits of the
@@ -57,7 +60,7 @@ template <> struct Eight<float> {
   __device__ __forceinline__ uint32_t amax(const float (&v)[8]) const { return mx_amax8(v); }
 };
 
-// item / tile_cols, for items < 16 tile_cols + 64: exact with recip =
+// item / tile_cols, for items < 8 tile_cols + 64: exact with recip =
 // ceil(2^32 / tile_cols) while item * tile_cols < 2^32 (tile_cols <= 2^13)
 __device__ __forceinline__ int row_of(int item, int tile_cols, uint32_t recip) {
   return tile_cols == 1 ? item : (int)__umulhi((uint32_t)item, recip);
@@ -75,43 +78,58 @@ __global__ void __launch_bounds__(kThreads)
                        int rows_per_cta) {
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  const int lane = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
   const int row0 = blockIdx.x * rows_per_cta;
   const int items = min(rows_per_cta, padded_rows - row0) * tile_cols;
   const T* x = reinterpret_cast<const T*>(a.x);
-  // every half warp makes the same number of passes (the shuffles need whole warps)
-  for (int i0 = 0; i0 < items; i0 += kUnroll * kHalfWarps) {
-    Eight<T> x8[kUnroll];
-    int row[kUnroll], tc[kUnroll];
-    bool in[kUnroll];
+  // every warp makes the same number of passes (the shuffles need whole warps)
+  for (int i0 = 0; i0 < items; i0 += kTilesAhead * kTeams) {
+    Eight<T> x8[kTilesAhead][2];
+    int row[kTilesAhead], tc[kTilesAhead];
+    bool in[kTilesAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int item = i0 + u * kHalfWarps + hw;
+    for (int u = 0; u < kTilesAhead; ++u) {
+      const int item = i0 + u * kTeams + team;
       const int r = row_of(item, tile_cols, recip);
       row[u] = row0 + r;
       tc[u] = item - r * tile_cols;
-      const int col = tc[u] * 128 + lane * 8;
+      const int col = tc[u] * 128 + lane * 16;
       in[u] = item < items && row[u] < a.rows && col < a.k;
-      x8[u].clear();
-      if (in[u]) x8[u].load(x + (size_t)row[u] * a.k + col);
+      x8[u][0].clear();
+      x8[u][1].clear();
+      if (in[u]) {
+        const T* p = x + (size_t)row[u] * a.k + col;
+        x8[u][0].load(p);
+        x8[u][1].load(p + 8);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int item = i0 + u * kHalfWarps + hw;
-      uint2 q;
-      float v[8];
-      x8[u].values(v);
-      const uint32_t byte = mx_encode8<FMT>(v, x8[u].amax(v), &q);
+    for (int u = 0; u < kTilesAhead; ++u) {
+      const int item = i0 + u * kTeams + team;
+      float v[2][8];
+      x8[u][0].values(v[0]);
+      x8[u][1].values(v[1]);
+      uint32_t amax = max(x8[u][0].amax(v[0]), x8[u][1].amax(v[1]));
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      const uint32_t byte = mx_scale_byte<FMT>(amax);
+      const float inv = mx_inverse(byte);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[h][j] *= inv;
       if (in[u]) {
-        const size_t vec = ((size_t)row[u] * a.k + tc[u] * 128 + lane * 8) / 8;
-        if constexpr (FMT == WQL_MX_FP4)
-          reinterpret_cast<uint32_t*>(a.codes)[vec] = q.x;
-        else
-          reinterpret_cast<uint2*>(a.codes)[vec] = q;
+        const size_t vec = ((size_t)row[u] * a.k + tc[u] * 128 + lane * 16) / 16;
+        if constexpr (FMT == WQL_MX_FP4) {
+          const uint2 q = make_uint2(mx_codes_fp4(v[0]), mx_codes_fp4(v[1]));
+          reinterpret_cast<uint2*>(a.codes)[vec] = byte == 255u ? make_uint2(0u, 0u) : q;
+        } else {
+          const uint2 q0 = mx_codes_fp8(v[0]), q1 = mx_codes_fp8(v[1]);
+          reinterpret_cast<uint4*>(a.codes)[vec] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+        }
       }
-      if ((lane & 3) == 0 && item < items)
+      if ((lane & 1) == 0 && item < items)
         reinterpret_cast<uint8_t*>(a.scales)[mx_scale_at(row[u], tc[u], tile_cols) +
-                                             (lane >> 2)] = (uint8_t)byte;
+                                             (lane >> 1)] = (uint8_t)byte;
     }
   }
 }
@@ -195,10 +213,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Rows per block: enough blocks for a few per SM, at most 16 rows each.
+// Rows per block: enough blocks for a few per SM, at most 8 rows each.
 int rows_per_cta(int rows) {
   const int r = rows / (device_sm_count() * 8);
-  return r < 1 ? 1 : r > 16 ? 16 : r;
+  return r < 1 ? 1 : r > 8 ? 8 : r;
 }
 
 template <typename T>
