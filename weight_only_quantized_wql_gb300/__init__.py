@@ -1,8 +1,10 @@
 """Weight-only quantised lm_head logits on GB300 -- Python binding of libwql.
 
-Thin ctypes wrappers with the C ABI's names (``include/wql.h``).  They only
-marshal arguments: torch tensors supply device memory and the current CUDA
-stream, and every step of the computation runs in libwql's CUDA kernels.
+Thin wrappers with the C ABI's names (``include/wql.h``), through ctypes or,
+for the operators around the head, a compiled module (``csrc/binding.cpp``:
+their smallest calls are bound by the host).  They only marshal arguments: torch
+tensors supply device memory and the current CUDA stream, and every step of the
+computation runs in libwql's CUDA kernels.
 There is no CPU or PyTorch fallback: if the library cannot be loaded, or a
 tensor is not on a CUDA device, the call raises.
 
@@ -25,6 +27,7 @@ Functions
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -438,6 +441,25 @@ def wql_embed_gather(ids: torch.Tensor, qw: QuantizedWeight, out_dtype=torch.flo
     return out.reshape(*ids.shape, qw.k)
 
 
+_native = None
+
+
+def _binding():
+    """The compiled wrappers (building and loading what is missing)."""
+    global _native
+    if _native is None:
+        load()
+        with _lock:
+            if _native is None:
+                if not os.path.exists(_build.BINDING):
+                    raise RuntimeError(f"{_build.BINDING} not found; run __graft_entry__.build()")
+                spec = importlib.util.spec_from_file_location("_wql_torch", _build.BINDING)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _native = module
+    return _native
+
+
 @dataclass
 class MXMatrix:
     """A matrix in microscaled codes, in the layout wql.h documents (wql_mx)."""
@@ -447,9 +469,8 @@ class MXMatrix:
     rows: int
     k: int
 
-    def _struct(self) -> _WqlMx:
-        return _WqlMx(self.fmt, 0, self.rows, self.k, self.codes.data_ptr(),
-                      self.scales.data_ptr())
+    def _fields(self):
+        return self.codes, self.scales, self.fmt, self.rows, self.k
 
     def nbytes(self) -> int:
         return self.codes.numel() + self.scales.numel()
@@ -459,79 +480,16 @@ def wql_mx_scale_bytes(rows: int, k: int) -> int:
     return int(load().wql_mx_scale_bytes(rows, k))
 
 
-def _rows(x: torch.Tensor, name: str):
-    """(rows, columns) of a contiguous CUDA tensor, leading dimensions
-    flattened -- from its sizes, since a view costs as much as a launch."""
-    if not (x.is_cuda and x.is_contiguous()):
-        _cuda(x, name)
-    k = x.shape[-1]
-    if x.dim() == 2:
-        return x.shape[0], k
-    return (x.numel() // k if k else 0), k
-
-
-def _same(t: torch.Tensor, name: str, x: torch.Tensor, numel: int):
-    """t lies on x's device, contiguous, in x's dtype, with numel elements."""
-    if not (t.is_cuda and t.is_contiguous()):
-        _cuda(t, name)
-    if t.dtype != x.dtype or t.numel() != numel or t.get_device() != x.get_device():
-        raise ValueError(f"{name} must be a {x.dtype} tensor of {numel} elements on {x.device}")
-
-
-if _raw_stream is not None:
-    def _stream_of(t: torch.Tensor) -> int:
-        return _raw_stream(t.get_device())
-else:
-    def _stream_of(t: torch.Tensor) -> int:
-        return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _mx_empty(rows: int, k: int, fmt: int, device) -> MXMatrix:
-    if fmt != MX_FP4 and fmt != MX_FP8:
-        raise ValueError("fmt must be MX_FP4 or MX_FP8")
-    codes = torch.empty((rows, k // 2 if fmt == MX_FP4 else k), dtype=torch.uint8, device=device)
-    scales = torch.empty(((rows + 127) // 128, (k + 127) // 128, 512), dtype=torch.uint8,
-                         device=device)
-    return MXMatrix(codes, scales, fmt, rows, k)
-
-
-def _mx_check(a: MXMatrix, name: str):
-    for t, part in ((a.codes, "codes"), (a.scales, "scales")):
-        if not (t.is_cuda and t.is_contiguous()):
-            _cuda(t, f"{name}.{part}")
-        if t.dtype != torch.uint8:
-            raise ValueError(f"{name}.{part} must be uint8")
-    if a.codes.numel() != a.rows * (a.k // 2 if a.fmt == MX_FP4 else a.k):
-        raise ValueError(f"{name}.codes does not hold {a.rows} x {a.k} codes")
-    if a.scales.numel() != (a.rows + 127) // 128 * ((a.k + 127) // 128) * 512:
-        raise ValueError(f"{name}.scales does not hold the scale tiles of {a.rows} x {a.k}")
-    if a.codes.get_device() != a.scales.get_device():
-        raise ValueError(f"{name}'s codes and scales must lie on one device")
-
-
 def wql_mx_quantize(x: torch.Tensor, fmt: int = MX_FP4) -> MXMatrix:
     """Microscaled codes of x (fp32/fp16/bf16); leading dimensions are
     flattened to rows (see wql.h)."""
-    lib = _lib or load()
-    rows, k = _rows(x, "x")
-    a = _mx_empty(rows, k, fmt, x.device)
-    status = lib.wql_mx_quantize(x.data_ptr(), _DTYPE_CODE[x.dtype], rows, k, fmt,
-                                 a.codes.data_ptr(), a.scales.data_ptr(), _stream_of(x))
-    if status:
-        raise WQLError("wql_mx_quantize", status)
-    return a
+    codes, scales, rows, k = (_native or _binding()).mx_quantize(x, fmt)
+    return MXMatrix(codes, scales, fmt, rows, k)
 
 
 def wql_mx_dequantize(a: MXMatrix, out_dtype=torch.float32) -> torch.Tensor:
     """The values [rows, k] that microscaled codes stand for."""
-    lib = _lib or load()
-    _mx_check(a, "a")
-    out = torch.empty((a.rows, a.k), dtype=out_dtype, device=a.codes.device)
-    status = lib.wql_mx_dequantize(ctypes.byref(a._struct()), _DTYPE_CODE[out_dtype],
-                                   out.data_ptr(), _stream_of(a.codes))
-    if status:
-        raise WQLError("wql_mx_dequantize", status)
-    return out
+    return (_native or _binding()).mx_dequantize(a._fields(), out_dtype)
 
 
 def wql_mx_logits(x: MXMatrix, w: MXMatrix, out_dtype=torch.bfloat16,
@@ -540,28 +498,9 @@ def wql_mx_logits(x: MXMatrix, w: MXMatrix, out_dtype=torch.bfloat16,
     """logits [x.rows, w.rows] of a microscaled head: x MX_FP8 or MX_FP4, w
     MX_FP4 (see wql.h).  With a workspace, a wait that runs out is recorded in
     its error word."""
-    lib = _lib or load()
-    _mx_check(x, "x")
-    _mx_check(w, "w")
-    if x.codes.get_device() != w.codes.get_device():
-        raise ValueError("x and w must lie on one device")
-    if out is None:
-        out = torch.empty((x.rows, w.rows), dtype=out_dtype, device=x.codes.device)
-    else:
-        _cuda(out, "out")
-        if out.dtype != out_dtype or out.numel() != x.rows * w.rows:
-            raise ValueError("out must be [x.rows, w.rows] of out_dtype")
-    if bias is not None:
-        _same(bias, "bias", out, w.rows)
     ws = workspace.get(wql_workspace_size(x.rows, w.rows, 0)) if workspace is not None else None
-    status = lib.wql_mx_logits(
-        ctypes.byref(x._struct()), ctypes.byref(w._struct()),
-        None if bias is None else bias.data_ptr(), _DTYPE_CODE[out_dtype], out.data_ptr(),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-        _stream_of(x.codes))
-    if status:
-        raise WQLError("wql_mx_logits", status)
-    return out
+    y = (_native or _binding()).mx_logits(x._fields(), w._fields(), out_dtype, bias, out, ws)
+    return y if out is None else out
 
 
 def wql_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
@@ -572,45 +511,12 @@ def wql_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor
     residual, unless one is passed; it may be `residual` itself).  y is in x's
     dtype (NORM_SAME, scales None), float8_e4m3fn with a float32 scale per row
     (NORM_E4M3), or an MXMatrix (NORM_MX_FP8 / NORM_MX_FP4, scales None)."""
-    lib = _lib or load()
-    m, k = _rows(x, "x")
-    _same(gamma, "gamma", x, k)
-    if residual is not None:
-        _same(residual, "residual", x, m * k)
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-    if residual_out is not None and residual_out is not residual:
-        _same(residual_out, "residual_out", x, m * k)
-    scales = scales_ptr = None
-    if fmt == NORM_SAME:
-        y = torch.empty_like(x)
-        y_ptr = y.data_ptr()
-    elif fmt == NORM_E4M3:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        y_ptr, scales_ptr = y.data_ptr(), scales.data_ptr()
-    elif fmt in (NORM_MX_FP8, NORM_MX_FP4):
-        y = _mx_empty(m, k, MX_FP8 if fmt == NORM_MX_FP8 else MX_FP4, x.device)
-        y_ptr, scales_ptr = y.codes.data_ptr(), y.scales.data_ptr()
-    else:
-        raise ValueError("fmt must be one of NORM_SAME, NORM_E4M3, NORM_MX_FP8, NORM_MX_FP4")
-    status = lib.wql_add_rmsnorm(
-        x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(),
-        _DTYPE_CODE[x.dtype], m, k, eps, fmt, y_ptr, scales_ptr,
-        None if residual_out is None else residual_out.data_ptr(), _stream_of(x))
-    if status:
-        raise WQLError("wql_add_rmsnorm", status)
-    return y, residual_out, scales
-
-
-def _row_param(t, name: str, dtype, m: int, logits: torch.Tensor):
-    if t is None:
-        return None
-    if not (t.is_cuda and t.is_contiguous()):
-        _cuda(t, name)
-    if t.dtype != dtype or t.numel() != m or t.get_device() != logits.get_device():
-        raise ValueError(f"{name} must be a {dtype} tensor of {m} elements on {logits.device}")
-    return t.data_ptr()
+    y, h, scales, tiles = (_native or _binding()).add_rmsnorm(x, gamma, residual, eps, fmt,
+                                                              residual_out)
+    if tiles is not None:
+        k = x.shape[-1]
+        y = MXMatrix(y, tiles, MX_FP8 if fmt == NORM_MX_FP8 else MX_FP4, x.numel() // k, k)
+    return y, (h if residual_out is None else residual_out), scales
 
 
 def wql_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -619,21 +525,4 @@ def wql_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor 
     """(ids int32, logp float32) drawn from each row of logits [*, n] with the
     random number u in [0, 1) of that row; the filters are tensors with a value
     per row (see wql.h).  A row without a logit above -inf gives (-1, NaN)."""
-    lib = _lib or load()
-    m, n = _rows(logits, "logits")
-    if u is None:
-        raise ValueError("u must be given")
-    f32 = torch.float32
-    shape, dev = logits.shape[:-1], logits.device
-    pu = _row_param(u, "u", f32, m, logits)
-    pt = _row_param(temperature, "temperature", f32, m, logits)
-    pk = _row_param(top_k, "top_k", torch.int32, m, logits)
-    pp = _row_param(top_p, "top_p", f32, m, logits)
-    pm = _row_param(min_p, "min_p", f32, m, logits)
-    ids = torch.empty(shape, dtype=torch.int32, device=dev)
-    logp = torch.empty(shape, dtype=f32, device=dev)
-    status = lib.wql_sample(logits.data_ptr(), _DTYPE_CODE[logits.dtype], m, n, pu, pt, pk, pp, pm,
-                            ids.data_ptr(), logp.data_ptr(), _stream_of(logits))
-    if status:
-        raise WQLError("wql_sample", status)
-    return ids, logp
+    return (_native or _binding()).sample(logits, u, temperature, top_k, top_p, min_p)

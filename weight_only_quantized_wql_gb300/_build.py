@@ -1,7 +1,9 @@
-"""Build libwql.so in-tree with nvcc for sm_103a (no cmake, no torch ext).
+"""Build libwql.so in-tree with nvcc for sm_103a, and the compiled half of the
+Python binding with g++ (no cmake).
 
 Each .cu file is compiled in its own nvcc process (in parallel), then linked
-with ``nvcc -shared``.  The result lands in ``_build/libwql.so`` beside this
+with ``nvcc -shared``; ``binding.cpp`` against the torch that is installed.  The
+results land in ``_build/libwql.so`` and ``_build/_wql_torch.so`` beside this
 file; rebuilt only when a source or header is newer.
 """
 from __future__ import annotations
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libwql.so")
+BINDING = os.path.join(BUILD, "_wql_torch.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -35,13 +40,14 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "wql.h")]
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "wql.h"),
+                                                                BINDING_SRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -64,14 +70,42 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout, r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:
+    def compile_binding() -> str:
+        import torch
+        torch_inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        obj = os.path.join(BUILD, "binding.o")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+        inc = [torch_inc, os.path.join(torch_inc, "torch", "csrc", "api", "include"), cuda,
+               sysconfig.get_paths()["include"], INCLUDE]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-DTORCH_EXTENSION_NAME=_wql_torch", *(f"-I{i}" for i in inc)]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr[-4000:]}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=min(9, len(sources()) + 1)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    # the library beside it is found by name, so that both are one instance
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, f"-L{BUILD}", "-l:libwql.so",
+           "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}", "-ltorch", "-ltorch_cpu", "-ltorch_python",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
