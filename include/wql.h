@@ -398,7 +398,8 @@ wql_status wql_add_rmsnorm(const void* x, const void* residual, const void* gamm
  *   r; logp = log(W_id / sum).
  * A row without a logit above -inf gives id -1 and logp NaN.  (Tokens less
  * likely than 2^-31 of the likeliest have W = 0 and are never drawn.)
- *   logits       device [m, n] of dtype (F32, F16 or BF16), 16-byte aligned
+ *   logits       device [m, n] of dtype (F32, F16 or BF16), aligned to its
+ *                elements
  *   u            device float [m], in [0, 1)
  *   temperature  device float [m], or NULL: 1
  *   top_k        device int32 [m], or NULL: off

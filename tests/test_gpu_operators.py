@@ -446,6 +446,22 @@ def test_sample_real_logits(mode, m, n, dt):
         assert ok, f"row {i}: token {int(ids[i])}, kept {lo}..{hi}"
 
 
+@pytest.mark.parametrize("n", [9, 4096, 40001, 200000])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_sample_any_alignment(n, dt):
+    """Logits that start on any element draw what aligned ones do."""
+    m = 3
+    l = (3 * torch.randn(m, n, generator=gen(n))).to(T[dt]).to(DEV)
+    u = torch.rand(m, generator=gen(1))
+    for k, p, mp in ((None, None, None), (20, 0.9, None), (None, 0.95, 0.001), (n // 2, 0.99, None)):
+        want = run_sample(l, u, 0.9, k, p, mp)
+        for shift in (1, 3, 7):
+            off = torch.empty(l.numel() + shift, dtype=l.dtype, device=DEV)[shift:].view(m, n)
+            off.copy_(l)
+            got = run_sample(off, u, 0.9, k, p, mp)
+            assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 def test_sample_follows_the_distribution():
     """20000 draws of one row: each token's share within 5 standard deviations."""
     m, n = 20000, 12

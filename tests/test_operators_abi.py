@@ -132,7 +132,8 @@ def test_sample_refusals(lib):
     assert call(dt=3) == EUNSUPPORTED
     assert call(n=wql.SAMPLE_MAX_N + 1) == EUNSUPPORTED
     assert call(m=1 << 27) == EUNSUPPORTED
-    assert call(l=A + 2) == EUNSUPPORTED
+    assert call(l=A + 1) == EUNSUPPORTED
+    assert call(l=A + 2, dt=F32) == EUNSUPPORTED
     assert call(t=A + 2) == EUNSUPPORTED
     assert call(k=A + 1) == EUNSUPPORTED
     assert call(m=0, l=None, u=None, ids=None) == OK

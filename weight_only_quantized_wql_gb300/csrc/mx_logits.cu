@@ -50,6 +50,7 @@ constexpr int kCodeBytes = kTileRows * kCols / 2;  // of the weight, in HBM
 constexpr int kProducerWarp = 0, kMmaWarp = 1, kEpilogueWarp0 = 2, kEpilogueWarps = 8;
 constexpr int kTokenWarp = kEpilogueWarp0 + kEpilogueWarps;
 constexpr int kCopyWarp0 = kTokenWarp + 1, kCopyWarps = 4;
+constexpr int kAheadStages = 4;                    // of the weight, prefetched into L2
 constexpr int kMaxResident = 24;                   // stages' worth of tokens that may stay
 constexpr int kMaxCopyDepth = 3;                   // stages of copies in flight per copying thread
 constexpr int kMaxStages = 12, kMinStages = 2;
@@ -103,6 +104,21 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// The same boxes, and a stretch of bytes, into L2 only.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map),
+               "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_bytes(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
@@ -261,6 +277,22 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // The kernel before this one (it may be writing X) is still running: bring
+  // the weight's first stages into L2 meanwhile, where a write of it would
+  // still be seen.
+  if (!COPY && warp == kProducerWarp && lane == 0) {
+    prefetch_tmap(&tw);
+    for (int i = 0; i < min(steps, kAheadStages); ++i) {
+      const int t = t0 + i / p.stages_k, c = i % p.stages_k;
+      if constexpr (K::kFp8)
+        prefetch_3d(&tw, 0, t * kTileRows, c * K::kBlocks);
+      else
+        prefetch_2d(&tw, c * 32, t * kTileRows);
+      prefetch_bytes(reinterpret_cast<const uint8_t*>(a.w_scales) +
+                         ((size_t)t * p.tile_cols + c * kTiles) * kMxTileBytes,
+                     (uint32_t)(min(kTiles, p.tile_cols - c * kTiles) * kMxTileBytes));
+    }
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -272,7 +304,6 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
   if (warp == kProducerWarp) {
     // ---------------- TMA: the weight and its scales ----------------
     if (lane == 0) {
-      if (!COPY) prefetch_tmap(&tw);
       const uint8_t* wsc = reinterpret_cast<const uint8_t*>(a.w_scales);
       int fills = 0, slot = 0;
       uint32_t phase = 0;

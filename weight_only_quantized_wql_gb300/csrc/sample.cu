@@ -887,7 +887,14 @@ __device__ __forceinline__ int batches_per_stretch(int q0, int q1) {
   return ((q1 - q0 + kBatch - 1) / kBatch + kSegs - 1) / kSegs;
 }
 
-// f(first piece, one past the last) -> this lane's sum, for every stretch of
+// Sums of weights' high and low 16 bits.  A stretch has at most 128 tokens of a
+// lane (2^20 over 16 warps, 16 stretches and 32 lanes), so a warp's sums of
+// them stay below 2^32.
+struct Sums {
+  uint32_t high, low;
+};
+
+// f(first piece, one past the last) -> this lane's sums, for every stretch of
 // this warp; the warp's sums go to sh.seg.
 template <typename F>
 __device__ __forceinline__ void sum_stretches(int q0, int q1, int per, F f) {
@@ -896,8 +903,10 @@ __device__ __forceinline__ void sum_stretches(int q0, int q1, int per, F f) {
   const int step = per * 32 * kShares;
   int seg = 0;
   for (int b = q0; b < q1; b += step, ++seg) {
-    const u64 s = warp_sum(f(b, min(q1, b + step)));
-    if (lane == 0) sh.seg[warp][seg] = s;
+    const Sums s = f(b, min(q1, b + step));
+    const uint32_t high = __reduce_add_sync(0xFFFFFFFFu, s.high);
+    const uint32_t low = __reduce_add_sync(0xFFFFFFFFu, s.low);
+    if (lane == 0) sh.seg[warp][seg] = ((u64)high << 16) + low;
   }
 }
 
@@ -912,7 +921,7 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
   const float lowest = rank_logit(cut);
   const int per = batches_per_stretch(q0, q1);
   sum_stretches(q0, q1, per, [&](int b0, int b1) {
-    u64 mine = 0;
+    uint32_t high = 0, low = 0;
     if constexpr (CUT) {
       pc.template each_above<2>(b0, b1, lowest, [&](const float (&v)[V], int i0) {
 #pragma unroll
@@ -921,13 +930,13 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
               (v[j] == lowest && rank_key(v[j], (uint32_t)(i0 + j)) < cut))
             continue;
           const float e = Row::e(r.depth(v[j]));
-          mine += e >= r.min_p ? Row::weight(e) : 0u;
+          const uint32_t w = e >= r.min_p ? Row::weight(e) : 0u;
+          high += w >> 16;
+          low += w & 0xFFFFu;
         }
       });
     } else {
-      // sums of the halves, kOne and all, modulo 2^32: a stretch has fewer than
-      // 2^16 tokens of a lane, so the halves' own sums stay below it
-      uint32_t high = 0, low = 0, pieces = 0;
+      uint32_t pieces = 0;             // the halves' sums have kOne in them, modulo 2^32
       pc.each(b0, b1, [&](const float (&v)[V], int) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -941,9 +950,10 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
         ++pieces;
       });
       const uint32_t ones = pieces * (uint32_t)V * Row::kOne;
-      mine = ((u64)(high - ones) << 16) + (u64)(low - ones);
+      high -= ones;
+      low -= ones;
     }
-    return mine;
+    return Sums{high, low};
   });
   __syncthreads();
   draw_by_stretch<CUT>(a, row, pc, q0, q1, per, team, r, cut, u);
@@ -983,7 +993,7 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
       ++pieces;
     });
     const uint32_t ones = pieces * (uint32_t)V * Row::kOne;
-    return ((u64)(high_sum - ones) << 16) + (u64)(low_sum - ones);
+    return Sums{high_sum - ones, low_sum - ones};
   });
   team.sync();
   const u64 open = listed_by_all(team);
@@ -1290,7 +1300,8 @@ template <typename T>
 cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
   const int c = cluster_size(a.m, a.n);
   if ((size_t)a.n * sizeof(T) / c + 64 <= (size_t)kHeldBytes) return launch_h<T, kHeld>(a, c, s);
-  if (a.n % (16 / (int)sizeof(T)) == 0) return launch_h<T, kWhole>(a, c, s);
+  if (a.n % (16 / (int)sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0)
+    return launch_h<T, kWhole>(a, c, s);
   return launch_h<T, kRagged>(a, c, s);
 }
 

@@ -550,7 +550,7 @@ wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n, c
   if (m > 0 && (!logits || !u || !ids_out)) return WQL_EINVAL;
   if (dtype != WQL_F32 && !half_dtype(dtype)) return WQL_EUNSUPPORTED;
   if (n > WQL_SAMPLE_MAX_N || m >= (int64_t(1) << 27)) return WQL_EUNSUPPORTED;
-  if (!aligned(logits, 16) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+  if (!aligned(logits, dtype == WQL_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
       !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(ids_out, 4) || !aligned(logp_out, 4))
     return WQL_EUNSUPPORTED;
   if (m == 0) return WQL_OK;
