@@ -327,6 +327,8 @@ EXACT = [  # n, top_k, top_p, min_p, spread of the logits
     (5003, 0, 0.9, 0.0, 2), (5003, 2500, 0.6, 0.0, 3), (20011, 40, 0.95, 0.0, 30),
     (20011, 0, 0.9, 0.0, 3), (40001, 3000, 0.999, 0.0, 5), (40001, 10, 1.0, 0.0, 1),
     (40001, 0, 1e-9, 0.0, 8), (40001, 39999, 1.0, 0.0, 4), (40001, 0, 0.97, 2.0, 30),
+    # more equal logits than the lists hold: the descent over the rank key
+    (40001, 0, 0.6, 0.0, 1), (100003, 0, 0.97, 0.0, 2), (100003, 30000, 0.5, 0.0, 1),
 ]
 
 
