@@ -130,10 +130,10 @@ struct Row {
   float top;       // largest logit
   float c;         // log2e / temperature
   float min_p;     // 0: off
-  // log2 of a token's weight over the likeliest's, not below -1000, which a
-  // NaN becomes too (top and c are finite here)
+  // log2 of a token's weight over the likeliest's (top and c are finite here; a
+  // NaN stays, converts to weight 0 and compares false)
   __device__ __forceinline__ float depth(float l) const {
-    return fmaxf(__fmul_rn(__fsub_rn(l, top), c), -1000.f);
+    return __fmul_rn(__fsub_rn(l, top), c);
   }
   // 2^x; the same bits as exp2f() from -126 up, and W = 0 below -31 anyway
   static __device__ __forceinline__ float e(float x) {
@@ -146,7 +146,8 @@ struct Row {
   }
   // The same in two halves without the conversion, which shares the slow unit
   // with the exponential: floats 2^23 + W / 2^16 and 2^23 + W % 2^16 (each
-  // product is exact, each sum truncates), whose bits are kOne + the half.
+  // product is exact, each sum truncates), whose bits are kOne + the half.  Not
+  // for a NaN.
   static constexpr uint32_t kOne = 0x4B000000u;
   static __device__ __forceinline__ void halves(float e, uint32_t* high, uint32_t* low) {
     const float h = __fmaf_rz(e, 32768.f, 8388608.f);
@@ -595,14 +596,14 @@ template <bool COUNT, bool MASS> __device__ __forceinline__ void fold_hist() {
   }
 }
 
-// An addition in shared memory under a predicate (an if around atomicAdd()
-// becomes a branch per token).
-__device__ __forceinline__ void add_if(bool yes, uint32_t addr, uint32_t v) {
+// Additions in shared memory where x is above a limit (an if around
+// atomicAdd() becomes a branch per token).
+__device__ __forceinline__ void add_above(float x, float limit, uint32_t addr, uint32_t v) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
+      "setp.gt.f32 p, %2, %3;\n\t"
       "@p red.shared.add.u32 [%0], %1;\n\t}" ::"r"(addr),
-      "r"(v), "r"((uint32_t)yes)
+      "r"(v), "f"(x), "f"(limit)
       : "memory");
 }
 
@@ -649,9 +650,10 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1,
         uint32_t high, low;
         Row::halves(Row::e(x), &high, &low);
         const uint32_t h = hist_addr + Row::bin_if_weight(x) * (kCopies * 4);
-        add_if(x > -31.5f, h, low - Row::kOne);
-        add_if(high != Row::kOne, h + kHigh * 4, high - Row::kOne);
-        if (COUNT) add_if((high | low) != Row::kOne, h + kCount * 4, 1u);
+        // no weight from -31 down, no high half from -15 down
+        add_above(x, -31.5f, h, low - Row::kOne);
+        add_above(x, -15.5f, h + kHigh * 4, high - Row::kOne);
+        if (COUNT) add_above(x, -31.5f, h + kCount * 4, (high | low) != Row::kOne ? 1u : 0u);
       }
     });
   } else {
@@ -941,7 +943,7 @@ __device__ __noinline__ void draw_in_row(const SampleArgs& a, int row, const P& 
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           float e = Row::e(r.depth(v[j]));
-          if (MIN_P) e = e >= r.min_p ? e : 0.f;
+          e = MIN_P ? (e >= r.min_p ? e : 0.f) : fmaxf(e, 0.f);      // (a NaN: 0)
           uint32_t h, l;
           Row::halves(e, &h, &l);
           high += h;
