@@ -184,11 +184,11 @@ template <typename T, Mode MODE> struct Pieces {
   }
   // first piece of a warp's part
   __device__ __forceinline__ int first(int part, int parts) const {
-    return (int)((long long)pieces * part / parts);
+    return (int)((uint32_t)pieces * (uint32_t)part / (uint32_t)parts);     // 2^18 * 128 at most
   }
   // the part that piece q lies in: the last that starts at or before q
   __device__ __forceinline__ int part_of(int q, int parts) const {
-    return (int)((((long long)q + 1) * parts - 1) / pieces);
+    return (int)((((uint32_t)q + 1u) * (uint32_t)parts - 1u) / (uint32_t)pieces);
   }
   __device__ __forceinline__ uint4 load(int q) const {
     if constexpr (HELD) {
@@ -199,6 +199,12 @@ template <typename T, Mode MODE> struct Pieces {
       }
       return __ldg(reinterpret_cast<const uint4*>(base) + q);
     }
+  }
+  // an element of the row, of a piece that this block has
+  __device__ __forceinline__ float element(int idx) const {
+    const int at = idx + mis;
+    if constexpr (HELD) return to_f32(reinterpret_cast<const T*>(held_pieces())[at - s0 * V]);
+    return to_f32(base[at]);
   }
   // the first or last piece, element by element
   __device__ __noinline__ uint4 load_end(int q) const {
@@ -394,11 +400,12 @@ __device__ __forceinline__ int pow2_at_least(int v) {
   return p;
 }
 
-__device__ __forceinline__ void append(const Team& team, u64 key) {
-  Shared& sh = shared();
-  const uint32_t at = atomicAdd(&sh.listed, 1u);
+__device__ __forceinline__ void put(const Team& team, uint32_t at, u64 key) {
   // (a block alone goes on into the joined list)
   if (at < (uint32_t)(team.size > 1 ? kLocal : kOpen)) keys()[at] = key;
+}
+__device__ __forceinline__ void append(const Team& team, u64 key) {
+  put(team, atomicAdd(&shared().listed, 1u), key);
 }
 
 // Tokens listed by all blocks of the cluster; more than kOpen when they do not
@@ -978,6 +985,7 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
   sum_stretches(q0, q1, per, [&](int b0, int b1) {
     uint32_t high_sum = 0, low_sum = 0, pieces = 0;  // of halves, as in draw_in_row()
     pc.template each_above<2>(b0, b1, low, [&](const float (&v)[V], int i0) {
+      uint32_t open = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float x = r.depth(v[j]);
@@ -987,12 +995,21 @@ __device__ __noinline__ void draw_nucleus(const SampleArgs& a, int row, const P&
         Row::halves(b < f.bin && e >= r.min_p ? e : 0.f, &h, &l);
         high_sum += h;
         low_sum += l;
-        if (b == f.bin) {
-          const u64 key = rank_key(v[j], (uint32_t)(i0 + j));
-          if (key >= from && Row::weight(e) != 0u) append(team, key);
-        }
+        open |= (b == f.bin && e >= 0x1p-31f ? 1u : 0u) << j;
       }
       ++pieces;
+      if (open != 0u) {                // one addition to the list's length per piece
+        uint32_t at = from == 0ull ? atomicAdd(&sh.listed, (uint32_t)__popc(open)) : 0u;
+        for (; open != 0u; open &= open - 1u) {
+          const int idx = i0 + __ffs((int)open) - 1;
+          const u64 key = rank_key(pc.element(idx), (uint32_t)idx);
+          if (from != 0ull) {
+            if (key >= from) append(team, key);
+          } else {
+            put(team, at++, key);
+          }
+        }
+      }
     });
     const uint32_t ones = pieces * (uint32_t)V * Row::kOne;
     return Sums{high_sum - ones, low_sum - ones};
