@@ -17,22 +17,30 @@
 //    wants 16 e2m1 codes (8 bytes) at the start of each 16-byte unit; TMA
 //    spreads them so when rows are whole 128-column blocks, else four warps
 //    copy 8-byte pieces into that layout with cp.async.  (Stages of 128
-//    columns would free their slots sooner, but took 168 us where 256 take
-//    119, one e4m3 token on the 248320 x 5120 head: more copies to issue.)
+//    columns would free their slots sooner, but took 168 us where 256 took
+//    119, now 108, one e4m3 token on the 248320 x 5120 head: more copies to
+//    issue.)
 //  * One warp issues: tcgen05.cp spreads a stage's scales over tensor memory
 //    (the stored tiles are in the order it wants), then the stage's products;
 //    both run in issue order.
 //  * Eight warps read the accumulators, add the bias, round, and store through
-//    shared memory by TMA, whole 256-byte runs of a token's logits (directly
-//    for few tokens or rows that are not 16-byte aligned).
+//    shared memory by TMA, whole 256-byte runs of a token's logits: 32.1 us
+//    for 256 tokens on 151936 x 1024, 48 us straight from registers (which few
+//    tokens, and rows that are not 16-byte aligned, still do).
 //  * More than 128 tokens, when 128 of them fit shared memory next to a ring
 //    of 64 KB of weight: they stay there for the whole launch, and CTAs take
 //    slices of 128 in turn over the same vocab tiles, so the weight comes from
-//    HBM about once (256 tokens, 151936 x 1024, e2m1: 33.9 us, 38.6 us with
+//    HBM about once (256 tokens, 151936 x 1024, e2m1: 32.1 us, 38.8 us with
 //    256 tokens re-read per tile).  Longer rows re-read the tokens from L2 for
 //    every tile, up to 256 (e4m3: 128) at a time.
 //  * The weight and the tokens have a producing thread each: one thread for
 //    both was the limit where a stage takes more copies.
+//  * While the kernel before it still runs, the weight's first stages are
+//    prefetched into L2 (one token on 151936 x 1024, e2m1: 18.0 us, 18.6
+//    without; more than four stages ahead crowd the first real copies).
+//  * Measured: one token 12.2 us of bytes in about 16 us on 151936 x 1024, 90 to
+//    94 % of the measured copy rate on 248320 x 5120 up to 32 tokens, 2480
+//    TFLOP/s at 256 tokens (e2m1, K = 1024).
 //  * Every wait is bounded; on a timeout the CTA records it, drains its own
 //    copies and products, frees its tensor memory and returns.
 #include "mx.cuh"
@@ -689,7 +697,7 @@ cudaError_t launch_mx_logits(const MxLogitsArgs& a, cudaStream_t s) {
                : launch_t<WQL_MX_FP4, false, __nv_bfloat16>(a, s);
   // TMA spreads e2m1 codes over 16-byte units itself, for whole 128-column
   // blocks and 32-byte aligned codes: 32 tokens on the 248320 x 5120 head take
-  // 122 us so, 166 us with cp.async
+  // 113 us so, 190 us with cp.async
   if (a.k % 128 == 0 && reinterpret_cast<uintptr_t>(a.w_codes) % 32 == 0)
     return f16 ? launch_t<WQL_MX_FP8, false, __half>(a, s)
                : launch_t<WQL_MX_FP8, false, __nv_bfloat16>(a, s);
