@@ -30,9 +30,10 @@
 // loops over a row are kept short (one 16-byte piece a turn): unrolled by four
 // they were bound by instruction fetches.  Measured: 1 x 151936 bf16 top-k 11.6
 // us, temperature alone 9.4, a nucleus 20; 64 x 248320 fp32, temperature alone,
-// 31 us; 256 x 151936 bf16 top-k 32 us (2.4 TB/s), a nucleus 100 us.  Histograms keep 16 copies, one per lane and its half warp's
-// partner, so that a warp's additions hardly meet in a bank; a copy's sums (16
-// low and 15 high bits of the weights apart) stay below 2^32 for 2^20 tokens.
+// 31 us; 256 x 151936 bf16 top-k 32 us (2.4 TB/s), a nucleus 100 us.
+// Histograms keep 16 copies, one per lane and its half warp's partner, so that a
+// warp's additions hardly meet in a bank; a copy's sums (16 low and 15 high bits
+// of the weights apart) stay below 2^32 for 2^20 tokens.
 #include <cooperative_groups.h>
 #include <stddef.h>
 
