@@ -39,8 +39,8 @@
 //    prefetched into L2 (one token on 151936 x 1024, e2m1: 18.0 us, 18.6
 //    without; more than four stages ahead crowd the first real copies).
 //  * Measured: one token 12.2 us of bytes in 18.1 us on 151936 x 1024,
-//    its quantisation included, 90 to 94 % of the measured copy rate on 248320 x 5120 up to 32 tokens, 2480
-//    TFLOP/s at 256 tokens (e2m1, K = 1024).
+//    its quantisation included, 90 to 94 % of the measured copy rate on
+//    248320 x 5120 up to 32 tokens, 2480 TFLOP/s at 256 tokens (e2m1, K = 1024).
 //  * Every wait is bounded; on a timeout the CTA records it, drains its own
 //    copies and products, frees its tensor memory and returns.
 #include "mx.cuh"
