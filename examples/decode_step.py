@@ -105,7 +105,10 @@ def decode(batch: int, vocab: int, hidden: int, steps: int, graph: bool, seed: i
     torch.cuda.synchronize()
     if workspace.error_word():
         raise RuntimeError(f"a wait ran out: error word {workspace.error_word():#x}")
-    return torch.stack(tokens).cpu(), torch.stack(logps).cpu()
+    ids = torch.stack(tokens).cpu()
+    if (ids == -2).any():
+        raise RuntimeError("a wait of the sampler ran out")
+    return ids, torch.stack(logps).cpu()
 
 
 def main() -> None:

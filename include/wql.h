@@ -397,7 +397,9 @@ wql_status wql_add_rmsnorm(const void* x, const void* residual, const void* gamm
  *   lowest index at which the running sum over the kept W, by index, exceeds
  *   r; logp = log(W_id / sum).
  * A row without a logit above -inf gives id -1 and logp NaN.  (Tokens less
- * likely than 2^-31 of the likeliest have W = 0 and are never drawn.)
+ * likely than 2^-31 of the likeliest have W = 0 and are never drawn.)  A row
+ * whose logits did not arrive within the kernel's bounded wait for them gives
+ * id -2 and logp NaN.
  *   logits       device [m, n] of dtype (F32, F16 or BF16), aligned to its
  *                elements
  *   u            device float [m], in [0, 1)
@@ -422,11 +424,14 @@ const char* wql_status_string(wql_status status);
  * tensor-core work in flight, and from then on the top-K outputs of every
  * call on that workspace read index -1 and value NaN.
  *   budget_cycles  SM cycles a wait of the tensor-core kernels on a ring slot
- *                  or on data may take (0: the default, about 1 s); the
- *                  waits for a CTA's own copies keep the default
+ *                  or on data, or one of wql_sample on a row's logits, may take
+ *                  (0: the default, about 1 s); the waits for a CTA's own copies
+ *                  before it ends keep the default
  *   stall_mma      1: the tensor-core kernels' MMA warp first waits on a
  *                  barrier nothing arrives on, so that its budget runs out
- *                  and every other role's waits run out after it
+ *                  and every other role's waits run out after it; wql_sample's
+ *                  wait for a row's logits (where they are copied to shared
+ *                  memory) is on such a barrier too
  * Process-wide, for the calls launched after it; not for concurrent use.
  * (The decode kernel, m <= 16, has no waits.) */
 wql_status wql_debug_set_waits(int64_t budget_cycles, int32_t stall_mma);

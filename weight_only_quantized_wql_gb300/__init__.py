@@ -524,5 +524,6 @@ def wql_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor 
                min_p: torch.Tensor | None = None):
     """(ids int32, logp float32) drawn from each row of logits [*, n] with the
     random number u in [0, 1) of that row; the filters are tensors with a value
-    per row (see wql.h).  A row without a logit above -inf gives (-1, NaN)."""
+    per row (see wql.h).  A row without a logit above -inf gives (-1, NaN), one
+    whose logits a bounded wait did not see arrive (-2, NaN)."""
     return (_native or _binding()).sample(logits, u, temperature, top_k, top_p, min_p)

@@ -197,6 +197,8 @@ struct SampleArgs {
   const float* min_p;         // null: off
   int32_t* ids;
   float* logp;                // or null
+  long long wait_budget;      // SM cycles the wait for a slice's copies may take
+  int diag_stall;             // diagnostics: that wait is for a barrier nothing arrives on
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 

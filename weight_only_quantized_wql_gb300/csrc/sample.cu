@@ -72,6 +72,7 @@ struct alignas(16) Shared {
   u64 red[kWarps];
   float redf[kWarps];
   uint64_t bars[kChunks];
+  uint64_t stall;                      // diagnostics: nothing arrives here
   // read by the other blocks of the cluster
   u64 bin_mass[kBins];
   uint32_t bin_count[kBins];
@@ -1104,6 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   pc.s0 = pc.first(team.rank * kWarps, parts);
   if (threadIdx.x == 0) {
     for (int c = 0; c < kChunks; ++c) mbar_init(&sh.bars[c], 1);
+    mbar_init(&sh.stall, 1);
     sh.failed = 0;
     sh.listed = 0u;
     sh.digit = -1;
@@ -1149,7 +1151,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   r.c = fminf(__fdiv_rn(kLog2e, t), 3.402823466e38f);
 
   if constexpr (HELD) {
-    if (!mbar_wait(&sh.bars[warp / (kWarps / kChunks)], 0u)) sh.failed = 1;
+    uint64_t* bar = a.diag_stall ? &sh.stall : &sh.bars[warp / (kWarps / kChunks)];
+    if (!mbar_wait(bar, 0u, a.wait_budget)) sh.failed = 1;
     __syncwarp();
   }
 
@@ -1179,8 +1182,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   r.top = mx;
 
   if (failed || mx == __int_as_float(0xFF800000)) {    // nothing left
+    if (HELD && sh.failed && threadIdx.x == 0) {
+      // no copy may be in flight when the block ends: its shared memory goes to
+      // the next one (one more budget, for all of them)
+      const long long t0 = clock64();
+      for (int c = 0; c < kChunks; ++c) mbar_wait_since(&sh.bars[c], 0u, t0);
+    }
     if (team.rank == 0 && threadIdx.x == 0) {
-      a.ids[row] = -1;
+      a.ids[row] = failed ? -2 : -1;
       if (a.logp) a.logp[row] = __int_as_float(0x7FC00000);
     }
     team.sync();

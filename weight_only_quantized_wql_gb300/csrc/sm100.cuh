@@ -66,6 +66,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+// The same for waits that share one budget, counted from t0 = clock64().
+__device__ __forceinline__ bool mbar_wait_since(uint64_t* bar, uint32_t parity, long long t0,
+                                                long long budget = kWaitBudgetCycles) {
+  const long long left = budget - (clock64() - t0);
+  return mbar_wait(bar, parity, left > 0 ? left : 0);
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

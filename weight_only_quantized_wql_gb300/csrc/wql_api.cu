@@ -566,6 +566,8 @@ wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n, c
   a.min_p = min_p;
   a.ids = ids_out;
   a.logp = logp_out;
+  a.wait_budget = diag_wait_budget();
+  a.diag_stall = diag_stall_mma();
   const cudaError_t e = launch_sample(a, stream);
   return e == cudaSuccess ? WQL_OK : cuda_fail(e);
 }
