@@ -44,6 +44,7 @@
 //  * Every wait is bounded; on a timeout the CTA records it, drains its own
 //    copies and products, frees its tensor memory and returns.
 #include "mx.cuh"
+#include "ring.cuh"
 #include "sm100.cuh"
 
 namespace wql {
@@ -308,6 +309,16 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
   griddep_wait();
   const uint32_t tmem = *tmem_slot;
   bool bad = false;
+  // Every copy that a thread has issued lands before the CTA can finish.  Each
+  // producing thread waits for its own: when one of them gives up the other may
+  // get further, and nobody else waits for those copies.  (The arrivals of a
+  // role that gave up are missing, and this runs out too: one budget in all.)
+  auto drain_fills = [&](int fills) {
+    const long long since = clock64();
+    return drain_ring(fills, p.ring, [&](int s, uint32_t parity) {
+      return mbar_wait_since(&full[s], parity, since);
+    });
+  };
 
   if (warp == kProducerWarp) {
     // ---------------- TMA: the weight and its scales ----------------
@@ -333,10 +344,7 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
           ++fills;
           if (++slot == p.ring) { slot = 0; phase ^= 1u; }
         }
-      // every copy issued lands before the CTA can finish (when another role
-      // gave up, its arrivals are missing and this runs out too)
-      for (int s = 0; s < p.ring && s < fills; ++s)
-        if (!mbar_wait(&full[s], (uint32_t)(((fills - 1 - s) / p.ring) & 1))) bad = true;
+      bad = !drain_fills(fills) || bad;
     }
   } else if (warp == kTokenWarp) {
     // ---------------- TMA: the tokens and their scales ----------------
@@ -369,17 +377,17 @@ __global__ void __launch_bounds__(Kind<XFMT, COPY>::kWarps * 32, 1)
         for (int c = 0; c < p.stages_k && steps > 0; ++c)
           if (!mbar_wait(&x_full[c], 0u)) bad = true;
       } else {
-        int slot = 0, c = 0;
+        int slot = 0, c = 0, fills = 0;
         uint32_t phase = 0;
-        for (int i = 0; i < steps; ++i) {
-          if (i >= p.ring) bad = !mbar_wait(&empty[slot], phase ^ 1u, p.wait_budget);
+        for (; fills < steps; ++fills) {
+          if (fills >= p.ring) bad = !mbar_wait(&empty[slot], phase ^ 1u, p.wait_budget);
           if (bad) break;
           uint8_t* st = sm + slot * p.stage_bytes;
           load(c, st + p.off_x, st + p.off_xs, &full[slot]);
           if (++slot == p.ring) { slot = 0; phase ^= 1u; }
           if (++c == p.stages_k) c = 0;
         }
-        // (the other producer's last waits, on the same barriers, cover these copies)
+        bad = !drain_fills(fills) || bad;
       }
     }
   } else if (warp == kMmaWarp) {
