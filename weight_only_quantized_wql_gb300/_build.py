@@ -40,8 +40,9 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "wql.h"),
-                                                                BINDING_SRC]
+    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+            glob.glob(os.path.join(CSRC, "*.h")) +
+            [os.path.join(INCLUDE, "wql.h"), BINDING_SRC])
 
 
 def up_to_date() -> bool:

@@ -1097,22 +1097,19 @@ cudaError_t launch_t(const DecodeParams& p, size_t smem, int ctas, cudaStream_t 
   // per instantiation: raise the dynamic smem limit when a launch needs more,
   // and ask for the smallest shared-memory carveout that holds it, leaving
   // the rest of the SM's 256 KB to L1 (scale rows are read through L1)
-  static size_t configured = 0;
-  static int carveout = -1;
-  if (smem > configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    configured = smem;
-  }
+  static LargestPerDevice limit;
+  static LastPerDevice carveout;
+  cudaError_t e = allow_smem(limit, kern, smem);
+  if (e != cudaSuccess) return e;
+  int device = 0;
+  e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
   const int pct = (int)(((smem + 1024) * 100 + 228 * 1024 - 1) / (228 * 1024));
-  if (pct != carveout) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         pct > 100 ? 100 : pct);
-    if (e != cudaSuccess) return e;
-    carveout = pct;
-  }
-  const cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(warps_of(NT) * 32), smem, s, p);
+  e = carveout.want(device, pct > 100 ? 100 : pct, [kern](int share) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, share);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((unsigned)ctas), dim3(warps_of(NT) * 32), smem, s, p);
   note_launch();
   return e;
 }

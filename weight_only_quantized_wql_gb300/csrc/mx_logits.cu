@@ -682,12 +682,9 @@ cudaError_t launch_t(const MxLogitsArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   auto kern = mx_logits_kernel<XFMT, COPY, OT>;
-  static size_t configured = 0;
-  if (smem > configured) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured = smem;
-  }
+  static LargestPerDevice limit;
+  e = allow_smem(limit, kern, smem);
+  if (e != cudaSuccess) return e;
   int teams = device_sm_count() / p.slices;
   if (teams < 1) teams = 1;
   if (teams > p.tiles) teams = p.tiles;

@@ -1301,13 +1301,9 @@ cudaError_t launch_h(const SampleArgs& a, int c, cudaStream_t s) {
   const int slice = ((a.n + V - 1) / V + 1 + c - 1) / c + 1;     // pieces of a block, at most
   const size_t smem = sizeof(Shared) + (size_t)(MODE == kHeld ? slice : 2) * 16;
   auto kern = sample_kernel<T, MODE>;
-  static size_t configured = 0;
-  if (smem > configured) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured = smem;
-  }
+  static LargestPerDevice limit;
+  cudaError_t e = allow_smem(limit, kern, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.m * c);
   cfg.blockDim = dim3(kThreads);
@@ -1322,7 +1318,7 @@ cudaError_t launch_h(const SampleArgs& a, int c, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
   note_launch();
   return e;
 }

@@ -659,14 +659,10 @@ template <int BITS>
 cudaError_t tc_launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const TcParams& p,
                         size_t smem, int ctas, cudaStream_t s) {
   auto kern = tc_logits_kernel<BITS>;
-  static size_t configured = 0;
-  if (smem > configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    configured = smem;
-  }
-  const cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), smem, s, tw, tx, p);
+  static LargestPerDevice limit;
+  cudaError_t e = allow_smem(limit, kern, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), smem, s, tw, tx, p);
   note_launch();
   return e;
 }

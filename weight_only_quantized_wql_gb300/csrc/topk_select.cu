@@ -643,14 +643,10 @@ cudaError_t launch_t(const LogitsArgs& a, cudaStream_t s) {
   parts = max(1, min(parts, min(WQL_MAX_CTAS, (a.n + kMinRange - 1) / kMinRange)));
   const size_t smem = (size_t)kStages * kStepBytes + (size_t)a.k * 2;
   auto kern = topk_select_kernel<XT, KT>;
-  static size_t configured = 0;
-  if (smem > configured) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured = smem;
-  }
-  const cudaError_t e = launch_pdl(kern, dim3(a.m, parts), dim3(kThreads), smem, s, a, parts);
+  static LargestPerDevice limit;
+  cudaError_t e = allow_smem(limit, kern, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(a.m, parts), dim3(kThreads), smem, s, a, parts);
   note_launch();
   return e;
 }

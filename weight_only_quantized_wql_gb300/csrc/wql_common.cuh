@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "launch_limits.h"
 #include "wql.h"
 
 namespace wql {
@@ -439,6 +440,18 @@ __device__ __forceinline__ void griddep_wait() {
 }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Lets `kern` take `smem` bytes of dynamic shared memory on the current device.
+// `limit` is the kernel's own, for the life of the process.
+template <typename Kernel>
+cudaError_t allow_smem(LargestPerDevice& limit, Kernel kern, size_t smem) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  return limit.raise(device, smem, [kern](size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
 }
 
 template <typename... Params, typename... Args>
