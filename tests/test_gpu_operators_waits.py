@@ -40,3 +40,28 @@ def test_sample_wait_timeout_is_reported_and_recovers(m, n, dt):
         want = ref64.sample_exact(l[i].tolist(), LOG2E, 0, 1.0, 0.0, float(u[i]))
         assert int(ids[i]) == want[0]
     assert torch.isfinite(logp).all()
+
+
+def test_mx_logits_without_a_workspace_reports_its_waits():
+    x = wql.wql_mx_quantize(torch.randn(3, 512, device=DEV), wql.MX_FP8)
+    w = wql.wql_mx_quantize(torch.randn(1000, 512, device=DEV))
+    good = wql.wql_mx_logits(x, w)
+    ws = wql.default_workspace(DEV)
+    assert ws.error_word() == 0
+    wql.wql_debug_set_waits(BUDGET, True)
+    wql.wql_mx_logits(x, w)
+    wql.wql_debug_set_waits(0, False)
+    assert ws.error_word() == 8
+    ws.clear_error()
+    assert torch.equal(wql.wql_mx_logits(x, w), good) and ws.error_word() == 0
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                     # a stream has one of its own
+        assert wql.default_workspace(DEV) is not ws
+        assert wql.default_workspace() is wql.default_workspace(DEV)
+
+
+def test_mx_logits_refuses_a_workspace_elsewhere():
+    x = wql.wql_mx_quantize(torch.randn(3, 512, device=DEV))
+    w = wql.wql_mx_quantize(torch.randn(100, 512, device=DEV))
+    with pytest.raises(ValueError, match="workspace"):
+        wql.wql_mx_logits(x, w, workspace=wql.Workspace("cpu"))

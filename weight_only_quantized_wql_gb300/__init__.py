@@ -320,8 +320,15 @@ def wql_unpack(packed: torch.Tensor, k: int) -> torch.Tensor:
 
 
 def default_workspace(device=None) -> Workspace:
+    """The workspace of the calls on a device's current stream that are given
+    none; its error word tells of their waits."""
     dev = torch.device(device or "cuda")
-    return _default_ws.setdefault((dev, torch.cuda.current_stream(dev)), Workspace(dev))
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    key = (idx, _stream(dev).value)
+    ws = _default_ws.get(key)
+    if ws is None:
+        ws = _default_ws.setdefault(key, Workspace(torch.device("cuda", idx)))
+    return ws
 
 
 def wql_logits(x: torch.Tensor, qw: QuantizedWeight, bias: torch.Tensor | None = None,
@@ -496,8 +503,10 @@ def wql_mx_logits(x: MXMatrix, w: MXMatrix, out_dtype=torch.bfloat16,
                   bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   workspace: Workspace | None = None) -> torch.Tensor:
     """logits [x.rows, w.rows] of a microscaled head: x MX_FP8 or MX_FP4, w
-    MX_FP4 (see wql.h).  With a workspace, a wait that runs out is recorded in
-    its error word."""
+    MX_FP4 (see wql.h).  A wait that runs out is recorded in the workspace's
+    error word, default_workspace()'s when none is given."""
+    if workspace is None:
+        workspace = default_workspace(x.codes.device) if x.codes.is_cuda else None
     ws = workspace.get(wql_workspace_size(x.rows, w.rows, 0)) if workspace is not None else None
     y = (_native or _binding()).mx_logits(x._fields(), w._fields(), out_dtype, bias, out, ws)
     return y if out is None else out

@@ -125,6 +125,12 @@ Tensor mx_logits(const Matrix& x, const Matrix& w, at::ScalarType out_dtype,
   const wql_mx mx = checked(x, "x"), mw = checked(w, "w");
   const Tensor& codes = std::get<0>(x);
   if (codes.get_device() != std::get<0>(w).get_device()) refuse("x and w must lie on one device");
+  if (workspace) {
+    check_cuda(*workspace, "workspace");
+    if (workspace->scalar_type() != at::kByte ||
+        workspace->get_device() != codes.get_device())
+      refuse("workspace must hold bytes on cuda:" + std::to_string(codes.get_device()));
+  }
   const c10::cuda::CUDAGuard on(codes.device());
   Tensor y;
   if (out) {
