@@ -101,8 +101,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         if _lib is not None:
             return _lib
         path = _build.LIB
-        if build_if_missing and not _build.up_to_date():
-            _build.build()
+        if build_if_missing:
+            _build.build(binding=False)
         if not os.path.exists(path):
             raise RuntimeError(f"libwql.so not found at {path}; run __graft_entry__.build()")
         lib = ctypes.CDLL(path)
@@ -458,8 +458,7 @@ def _binding():
         load()
         with _lock:
             if _native is None:
-                if not os.path.exists(_build.BINDING):
-                    raise RuntimeError(f"{_build.BINDING} not found; run __graft_entry__.build()")
+                _build.build(library=False)
                 spec = importlib.util.spec_from_file_location("_wql_torch", _build.BINDING)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
