@@ -442,17 +442,34 @@ __device__ void join_lists(const Team& team) {
   __syncthreads();
 }
 
+// floor(f * s) for 0 < f < 1 and s < 2^52, and whether something is left of it:
+// exact in 128 bits (the product has up to 76 significant ones).
+__device__ __forceinline__ u64 floor_product(float f, u64 s, bool* rest) {
+  const uint32_t b = __float_as_uint(f);
+  const int exponent = max((int)(b >> 23), 1);         // f = mantissa * 2^(exponent - 150)
+  const u64 mantissa = (b & 0x7FFFFFu) | (b >> 23 ? 0x800000u : 0u);
+  const int shift = 150 - exponent;                    // 24 .. 149
+  const u64 lo = mantissa * s, hi = __umul64hi(mantissa, s);       // hi < 2^12
+  const int high_shift = min(shift - 64, 12);
+  *rest = shift < 64 ? (lo << (64 - shift)) != 0ull
+                     : lo != 0ull || (hi & ((1ull << high_shift) - 1ull)) != 0ull;
+  return shift < 64 ? (hi << (64 - shift)) | (lo >> shift) : hi >> high_shift;
+}
+
 // The integer that a nucleus' weights have to reach: those before a kept
-// token sum to less than p * sum, so to less than its ceiling.
+// token sum to less than p * sum, so to less than its ceiling (p < 1).
 __device__ __forceinline__ u64 nucleus_target(float p, u64 sum) {
-  const double t = ceil((double)p * (double)sum);
-  return t < 1.0 ? 1ull : (u64)t;
+  if (!(p > 0.f)) return 1ull;
+  bool rest;
+  const u64 t = floor_product(p, sum, &rest);
+  return max(t + (rest ? 1ull : 0ull), 1ull);
 }
 
 __device__ __forceinline__ u64 draw_target(float u, u64 sum) {
-  const double r = (double)u * (double)sum;
-  const u64 v = r > 0.0 ? (u64)r : 0ull;
-  return v < sum ? v : sum - 1;
+  if (!(u > 0.f)) return 0ull;
+  if (u >= 1.f) return sum - 1;
+  bool rest;
+  return floor_product(u, sum, &rest);
 }
 
 __device__ __forceinline__ void write_draw(const SampleArgs& a, int row, int id, uint32_t w,
