@@ -69,3 +69,25 @@ def test_nucleus_just_above_a_running_sum(dt, top_k, step):
     want, _, _ = ref64.sample_exact(l, LOG2E, top_k or 0, p, 0.0, 0.0)
     assert want == 0
     assert draw(l, dt, 0.0, top_k, p) == want
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,top_k,top_p,spread", [
+    (1000, 50, 1.0, 12), (1000, 0, 0.5, 12), (1000, 20, 0.8, 12), (5003, 2500, 0.6, 3),
+    (40001, 40, 0.95, 30), (40001, 0, 0.9, 3), (100003, 0, 0.6, 1), (100003, 30000, 0.5, 1)])
+def test_temperature_next_to_zero(n, top_k, top_p, spread, dt):
+    """c = 2^126 and logits that far below 1: four times c is no float."""
+    m, tiny = 4, 2.0 ** -126
+    t = LOG2E * tiny
+    assert float(np.float32(t)) == t
+    g = torch.Generator().manual_seed(n + top_k)
+    l = torch.randint(-spread, spread + 1, (m, n), generator=g).float() * tiny
+    u = torch.tensor([0.0, 0.3, 0.77, 1.0 - 2.0 ** -24])
+    full = lambda v, d=torch.float32: torch.full((m,), v, dtype=d, device=DEV)  # noqa: E731
+    ids, logp = wql.wql_sample(l.to(T[dt]).to(DEV), u.to(DEV), full(t), full(top_k, torch.int32),
+                               full(top_p))
+    for i in range(m):
+        want, w, total = ref64.sample_exact(l[i].tolist(), t, top_k, top_p, 0.0, float(u[i]))
+        assert int(ids[i]) == want
+        lp = np.log(w / total)
+        assert abs(float(logp[i]) - lp) <= 4 * 2.0 ** -24 + 2.0 ** -22 * abs(lp)

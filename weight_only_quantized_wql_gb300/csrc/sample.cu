@@ -739,13 +739,19 @@ __device__ __noinline__ bool search_round(const P& pc, int q0, int q1,
   return true;
 }
 
+// The distance below the maximum that is `bins` quarter octaves (4 * c may be
+// above the largest float, for a temperature next to zero).
+__device__ __forceinline__ float distance(const Row& r, float bins) {
+  return bins * 0.25f / r.c;
+}
+
 // Generous bounds of the logits of quarter octave `bin`: no token of it lies
 // outside, and none of a lower or higher one beyond the next.
 __device__ __forceinline__ float bin_low(const Row& r, int bin) {
-  return r.top - ((float)bin + 0.75f) / (4.f * r.c);
+  return r.top - distance(r, (float)bin + 0.75f);
 }
 __device__ __forceinline__ float bin_high(const Row& r, int bin) {
-  return r.top - ((float)bin - 0.75f) / (4.f * r.c);
+  return r.top - distance(r, (float)bin - 0.75f);
 }
 
 // The open tokens, joined and ranked by the first block: the rank key of the
@@ -1260,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const bool all = sh.digit < 0;
     // (a little below the edge, against the rounding here)
     const float bound = all ? __int_as_float(0xFF800000)
-                            : r.top - ((float)sh.digit + 0.5f + 1e-3f) / (4.f * r.c);
+                            : r.top - distance(r, (float)sh.digit + 0.5f + 1e-3f);
     pc.template each_above<4>(q0, q1, bound, [&](const float (&v)[V], int i0) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
