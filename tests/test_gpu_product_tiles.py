@@ -57,3 +57,28 @@ def test_many_tiles_per_block(fmt, m, n, k, dt):
         worst = max(worst, float((err / tol).max()))
     assert worst <= 1, f"worst {worst:.2f} of the tolerance"
     assert torch.equal(got, wql.wql_mx_logits(xa, wa, T[dt], bias=bias.to(DEV)))
+
+
+@pytest.mark.parametrize("fmt", [wql.MX_FP8, wql.MX_FP4])
+@pytest.mark.parametrize("m,n,k", [(5, 1000, 512), (40, 1000, 640), (200, 1000, 384)])
+def test_operands_and_output_on_other_boundaries(fmt, m, n, k):
+    """Codes 16 bytes into a buffer, logits two bytes into one: other copies, the
+    same logits."""
+    g = torch.Generator().manual_seed(n + k)
+    xa = wql.wql_mx_quantize(torch.randn(m, k, generator=g).to(DEV), fmt)
+    wa = wql.wql_mx_quantize(torch.randn(n, k, generator=g).to(DEV))
+    want = wql.wql_mx_logits(xa, wa, torch.float16)
+
+    def moved(a):
+        codes = torch.empty(a.codes.numel() + 16, dtype=torch.uint8, device=DEV)[16:].view(a.codes.shape)
+        scales = torch.empty(a.scales.numel() + 16, dtype=torch.uint8, device=DEV)[16:].view(a.scales.shape)
+        codes.copy_(a.codes)
+        scales.copy_(a.scales)
+        return wql.MXMatrix(codes, scales, a.fmt, a.rows, a.k)
+
+    buf = torch.full((m * n + 16,), 7.0, dtype=torch.float16, device=DEV)
+    out = buf[1:1 + m * n].view(m, n)
+    got = wql.wql_mx_logits(moved(xa), moved(wa), torch.float16, out=out)
+    # the same products in the same order of columns, whatever brings them in
+    assert torch.equal(got, want)
+    assert buf[0] == 7 and torch.all(buf[1 + m * n:] == 7)
