@@ -174,13 +174,15 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _stream_handle(idx: int) -> int:
+    """torch's current CUDA stream on a device (the raw handle, read the cheap
+    way when this torch build offers it)."""
+    return _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream(idx).cuda_stream
+
+
 def _stream(device) -> ctypes.c_void_p:
-    """torch's current CUDA stream on `device` (the raw handle, read the
-    cheap way when this torch build offers it)."""
-    if _raw_stream is not None:
-        idx = device.index if device.index is not None else torch.cuda.current_device()
-        return ctypes.c_void_p(_raw_stream(idx))
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_stream_handle(
+        device.index if device.index is not None else torch.cuda.current_device()))
 
 
 @dataclass
@@ -323,8 +325,11 @@ def default_workspace(device=None) -> Workspace:
     """The workspace of the calls on a device's current stream that are given
     none; its error word tells of their waits."""
     dev = torch.device(device or "cuda")
-    idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    key = (idx, _stream(dev).value)
+    return _default_workspace(dev.index if dev.index is not None else torch.cuda.current_device())
+
+
+def _default_workspace(idx: int) -> Workspace:
+    key = (idx, _stream_handle(idx))
     ws = _default_ws.get(key)
     if ws is None:
         ws = _default_ws.setdefault(key, Workspace(torch.device("cuda", idx)))
@@ -505,7 +510,8 @@ def wql_mx_logits(x: MXMatrix, w: MXMatrix, out_dtype=torch.bfloat16,
     MX_FP4 (see wql.h).  A wait that runs out is recorded in the workspace's
     error word, default_workspace()'s when none is given."""
     if workspace is None:
-        workspace = default_workspace(x.codes.device) if x.codes.is_cuda else None
+        idx = x.codes.get_device()
+        workspace = _default_workspace(idx) if idx >= 0 else None
     ws = workspace.get(wql_workspace_size(x.rows, w.rows, 0)) if workspace is not None else None
     y = (_native or _binding()).mx_logits(x._fields(), w._fields(), out_dtype, bias, out, ws)
     return y if out is None else out
