@@ -1127,14 +1127,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int q0 = pc.first(part, parts), q1 = pc.first(part + 1, parts);
   pc.s0 = pc.first(team.rank * kWarps, parts);
   if (threadIdx.x == 0) {
-    for (int c = 0; c < kChunks; ++c) mbar_init(&sh.bars[c], 1);
-    mbar_init(&sh.stall, 1);
+    if constexpr (HELD) {
+      for (int c = 0; c < kChunks; ++c) mbar_init(&sh.bars[c], 1);
+      mbar_init(&sh.stall, 1);
+    }
     sh.failed = 0;
     sh.listed = 0u;
     sh.digit = -1;
     sh.cut = 0ull;
     sh.sum = 0ull;
-    fence_barrier_init();
+    if constexpr (HELD) fence_barrier_init();
   }
   clear_hist();
   __syncthreads();
@@ -1200,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   bool failed = false;
   team.over(&sh.max, [&](float m, int) {
     mx = fmaxf(mx, m);
-    failed = failed || m != m;
+    if constexpr (HELD) failed = failed || m != m;
   });
   r.top = mx;
 
