@@ -1,7 +1,7 @@
 // binding.cpp -- the Python calls of the operators around the head: argument
 // checks, outputs from torch's allocator, torch's current stream, one call of
-// the C ABI.  No computation.  Through ctypes and Python the same call of
-// wql_add_rmsnorm cost the host 12 us, through this 7.6 us (a 1 x 1024 row, whose
+// the C ABI.  No computation.  Through ctypes and Python a call cost the host
+// 10 to 14 us, through this 5.5 to 8.5 us (a 1 x 1024 row's norm 12 and 8.2, whose
 // kernel takes 2): the smallest calls are bound by the host.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>

@@ -24,13 +24,13 @@
 //    (the stored tiles are in the order it wants), then the stage's products;
 //    both run in issue order.
 //  * Eight warps read the accumulators, add the bias, round, and store through
-//    shared memory by TMA, whole 256-byte runs of a token's logits: 32.1 us
+//    shared memory by TMA, whole 256-byte runs of a token's logits: 32.0 us
 //    for 256 tokens on 151936 x 1024, 48 us straight from registers (which few
 //    tokens, and rows that are not 16-byte aligned, still do).
 //  * More than 128 tokens, when 128 of them fit shared memory next to a ring
 //    of 64 KB of weight: they stay there for the whole launch, and CTAs take
 //    slices of 128 in turn over the same vocab tiles, so the weight comes from
-//    HBM about once (256 tokens, 151936 x 1024, e2m1: 32.1 us, 38.8 us with
+//    HBM about once (256 tokens, 151936 x 1024, e2m1: 32.0 us, 38.8 us with
 //    256 tokens re-read per tile).  Longer rows re-read the tokens from L2 for
 //    every tile, up to 256 (e4m3: 128) at a time.
 //  * The weight and the tokens have a producing thread each: one thread for
@@ -38,9 +38,10 @@
 //  * While the kernel before it still runs, the weight's first stages are
 //    prefetched into L2 (one token on 151936 x 1024, e2m1: 18.0 us, 18.6
 //    without; more than four stages ahead crowd the first real copies).
-//  * Measured: one token 12.2 us of bytes in 18.1 us on 151936 x 1024,
-//    its quantisation included, 90 to 94 % of the measured copy rate on
-//    248320 x 5120 up to 32 tokens, 2480 TFLOP/s at 256 tokens (e2m1, K = 1024).
+//  * Measured, the tokens' quantisation included (as in the figures above):
+//    one token 12.2 us of bytes in 18.1 us on 151936 x 1024 (17.1 us alone), 90 to
+//    94 % of the measured copy rate on 248320 x 5120 up to 32 tokens, 2490 TFLOP/s
+//    at 256 tokens (e2m1, K = 1024) and 4080 TFLOP/s (K = 5120).
 //  * Every wait is bounded; on a timeout the CTA records it, drains its own
 //    copies and products, frees its tensor memory and returns.
 #include "mx.cuh"

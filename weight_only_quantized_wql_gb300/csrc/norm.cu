@@ -6,8 +6,15 @@
 // bytes of y an element.  One block per row: the row stays in registers
 // between the sum of squares and the output, so every byte moves once.  Sums
 // and the norm are fp32; y is rounded once, to the output.  Measured: 4096 x 5120
-// bf16 to 16 bits 26.6 us (93 % of the copy rate), to e4m3 25.7 us (84 %), 1 x 1024
-// 1.9 us.
+// bf16 to 16 bits 26.6 us (93 % of the copy rate), to e4m3 25.7 us (84 %), to
+// microscaled e4m3 25.8 us (84 %), to e2m1 25.1 us (80 %); 1 x 1024 1.8 us, 32 x 5120
+// to microscaled e4m3 2.6 us.
+// Where a thread holds 64 elements (rows of more than 16384 when there are many,
+// else of more than 32768) the 64 registers of a 1024-thread block spill, 236 to 456
+// bytes a thread: 512 x 16384 bf16 to 16 bits takes 16.4 us (60 %), 512 x 16416 26.8
+// us (37 %), 512 x 65536 70.5 us (56 %).  By elements the spill is 2376 to 2660
+// bytes: 512 x 4096 off a 16-byte boundary takes 6.4 us, 512 x 16384 53 us, 512 x
+// 65536 431 us (9 %).
 #include "mx.cuh"
 
 namespace wql {

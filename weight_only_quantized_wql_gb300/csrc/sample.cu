@@ -25,12 +25,14 @@
 //    rank key at a time, until the open tokens fit; then, as when temperature
 //    or min-p alone is on, one pass for the stretches' sums and the walk.
 //
-// What bounds it: per weight some ten to twenty instructions, among them an
-// exponential and a conversion on the slow unit, and two or three passes.  The
-// loops over a row are kept short (one 16-byte piece a turn): unrolled by four
-// they were bound by instruction fetches.  Measured: 1 x 151936 bf16 top-k 11.6
-// us, temperature alone 9.4, a nucleus 20; 64 x 248320 fp32, temperature alone,
-// 31 us; 256 x 151936 bf16 top-k 32 us (2.4 TB/s), a nucleus 100 us.
+// What bounds it: one row, the barriers between its dependent steps; many rows,
+// the latency of two or three passes' loads (all but the first from L2) at 27 warps
+// an SM, and at 256 rows that 104 of 152 SMs have two of them: the schedulers issue
+// in 30 to 47 % of the cycles, shared memory's pipe is 11 % busy.  The loops over a
+// row are kept short (one 16-byte piece a turn): unrolled by four they were bound by
+// instruction fetches.  Measured: 1 x 151936 bf16 top-k 10.7 us, temperature alone
+// 9.3, a nucleus 19.2; 64 x 248320 fp32, temperature alone, 31 us; 256 x 151936 bf16
+// top-k 31 us (2.5 TB/s), a nucleus 100 us.
 // Histograms keep 16 copies, one per lane and its half warp's partner, so that a
 // warp's additions hardly meet in a bank; a copy's sums (16 low and 15 high bits
 // of the weights apart) stay below 2^32 for 2^20 tokens.
@@ -922,9 +924,10 @@ __device__ __forceinline__ int batches_per_stretch(int q0, int q1) {
   return ((q1 - q0 + kBatch - 1) / kBatch + kSegs - 1) / kSegs;
 }
 
-// Sums of weights' high and low 16 bits.  A stretch has at most 128 tokens of a
-// lane (2^20 over 16 warps, 16 stretches and 32 lanes), so a warp's sums of
-// them stay below 2^32.
+// Sums of weights' high and low 16 bits.  A stretch has at most 160 tokens of a
+// lane, 5120 of a warp: 2^20 logits of 16 bits off a 16-byte boundary are 2^17 + 1
+// pieces, of which one of 16 warps gets 8193, 65 batches, five a stretch.  So a
+// warp's sums of them stay below 2^29.
 struct Sums {
   uint32_t high, low;
 };
@@ -1313,7 +1316,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 // (two blocks fit one), with at least 4096 logits each.  (256 x 151936 bf16
 // with four blocks per row, so that shared memory holds them, takes 66 us for
 // top-k and 137 us for a nucleus, most of it in the clusters' barriers; with
-// one block per row 32 and 100.)
+// one block per row 31 and 100.)
 int cluster_size(int m, int n) {
   int c = 1;
   while (c < kMaxCluster && 2ll * c * m <= 2ll * device_sm_count() && n / (2 * c) >= 4096) c *= 2;
