@@ -414,6 +414,139 @@ wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n,
                       const float* top_p, const float* min_p, int32_t* ids_out,
                       float* logp_out, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Requests with adapters of their own, and beam search.  (No counterpart on
+ * the pages.)
+ * ------------------------------------------------------------------------- */
+
+/* Largest rank of an adapter; adapters of one set are fewer than this. */
+#define WQL_LORA_MAX_RANK 128
+#define WQL_LORA_MAX_COUNT (1 << 22)
+
+/* Low-rank adapters of one projection [n, k], laid out once; all of one rank
+ * (smaller ones are padded with zeros).
+ * Requirements: rank a multiple of 8, at most WQL_LORA_MAX_RANK; k % 8 == 0,
+ * k <= 2^20; n < 2^31; a and b 16-byte, scale 4-byte aligned. */
+typedef struct wql_lora {
+  int32_t dtype;        /* WQL_F16 or WQL_BF16: of a, b, x, y and out */
+  int32_t rank;
+  int64_t count;        /* adapters */
+  int64_t n;            /* rows of the projection (vocab) */
+  int64_t k;            /* hidden size */
+  const void* a;        /* device [count, rank, k] */
+  const void* b;        /* device [count, n, rank] */
+  const float* scale;   /* device float [count], or NULL: 1 */
+} wql_lora;
+
+/* Bytes of workspace wql_lora_add needs for m rows (0 for bad sizes).  Host
+ * arithmetic.  The buffer needs no preparation; calls that may run
+ * concurrently need separate ones. */
+size_t wql_lora_workspace_size(int64_t m, int32_t rank);
+
+/* Adds to the result of a shared projection what the adapter of each row's
+ * request adds to it: with i = ids[m],
+ *   out[m, n] = RN(y[m, n] + scale[i] * sum_j u[m, j] * b[i, n, j]),
+ *   u[m, j]   = sum_k x[m, k] * a[i, j, k],
+ * products exact or, for u, split into two parts of 16 bits (fp16: 22 bits
+ * below the row's largest |u|; bf16: 16 bits of each u), sums in fp32, rounded
+ * once.  A row whose id lies outside [0, count) has no adapter: out[m] = y[m].
+ * A value of a or b that is not finite makes what it is multiplied with
+ * infinite or NaN.
+ *   x    device [m, k], 16-byte aligned
+ *   ids  device int32 [m], in any order
+ *   y    device [m, n], aligned to its elements (16 bytes and n % 8 == 0 run
+ *        faster)
+ *   out  device [m, n]; y itself, or apart from it
+ *   workspace  device, 256-byte aligned, ws_bytes >= wql_lora_workspace_size(m,
+ *        rank); out must not overlap x, ids, the adapters or the workspace
+ * m <= 2^23. */
+wql_status wql_lora_add(const wql_lora* adapters, const void* x, int64_t m, const int32_t* ids,
+                        const void* y, void* out, void* workspace, size_t ws_bytes,
+                        cudaStream_t stream);
+
+/* Most beams of a sequence, and the largest vocabulary of wql_beam_select. */
+#define WQL_MAX_BEAMS 32
+#define WQL_BEAM_MAX_N (1 << 20)
+
+/* The slots that wql_beam_select gives the beams it selects. */
+typedef enum wql_beam_order {
+  WQL_BEAM_RANKED = 0,    /* by rank: slot 0 holds the best */
+  WQL_BEAM_ANCHORED = 1   /* the best continuation of every beam that has one takes that
+                             beam's slot, so that its states stay where they are; the others
+                             fill the free slots, by rank */
+} wql_beam_order;
+
+/* Bytes of workspace wql_beam_select needs (0 for bad sizes).  Host arithmetic.
+ * The buffer needs no preparation; calls that may run concurrently need
+ * separate ones. */
+size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n);
+
+/* One step of beam search for `batch` sequences of `beams` beams each.  The
+ * continuation of beam w by token v scores
+ *   s[w, v] = scores[w] + l[w, v] - log sum_v' exp(l[w, v']),
+ * l the logits: exponentials in fp32 over the row's largest logit, sums over a
+ * row's parts and scores in binary64, rounded to fp32 at the end.  Of a
+ * sequence's beams * n continuations the best `beams` whose token is not `eos`
+ * are selected: score descending, then beam ascending, then, within a beam,
+ * logit descending and token ascending.
+ *   A NaN logit counts as -inf; so does one of -inf give no continuation.  In a
+ *   row with logits of +inf those score scores[w] and no other continues.  A beam
+ *   whose score is not finite has no continuations.  Where fewer than `beams` are
+ *   left, the rest of the slots (the free ones in ascending order) get token -1,
+ *   parent -1 and score -inf.
+ *   logits       device [batch, beams, n] of dtype (F32, F16 or BF16), aligned to
+ *                its elements
+ *   scores       device float [batch, beams]: log-probabilities of the beams (for
+ *                a sequence's first step: 0, then -inf)
+ *   eos          the token that ends a sequence, or -1: none
+ *   tokens_out, parents_out  device int32 [batch, beams]: the token and the beam
+ *                (0 .. beams - 1) that each slot continues
+ *   scores_out   device float [batch, beams]; may be scores
+ *   ended_out    device float [batch, beams], or NULL: s[w, eos] by beam w where
+ *                fewer than `beams` continuations of the sequence (those by eos
+ *                among them) have a larger score; -inf elsewhere
+ *   workspace    device, 256-byte aligned, ws_bytes >= wql_beam_workspace_size()
+ * 1 <= beams <= WQL_MAX_BEAMS, 1 <= n <= WQL_BEAM_MAX_N, batch * beams <= 2^20. */
+wql_status wql_beam_select(const void* logits, int32_t dtype, int64_t batch, int64_t beams,
+                           int64_t n, const float* scores, int32_t eos, int32_t order,
+                           int32_t* tokens_out, int32_t* parents_out, float* scores_out,
+                           float* ended_out, void* workspace, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* Most states of one wql_beam_reorder call. */
+#define WQL_MAX_STATES 1024
+
+/* States of beams (a cache, a history of tokens): row r, block o, position p
+ * starts at data + r * row_stride + o * outer_stride + p * position_stride and
+ * is position_bytes long.  Strides in bytes, not negative. */
+typedef struct wql_state {
+  void* data;               /* device */
+  int64_t row_stride;
+  int64_t outer;            /* blocks of a row (heads, say) */
+  int64_t outer_stride;
+  int64_t positions;
+  int64_t position_stride;
+  int64_t position_bytes;
+} wql_state;
+
+/* Moves the states of beams to the slots of a selection, in place: for every
+ * state and sequence b,
+ *   row b * beams + j becomes what row b * beams + parents[b, j] was,
+ * in all blocks, in the first lengths[b] positions (limited to 0 .. positions)
+ * or, without lengths, in all.  Rows whose parent is outside 0 .. beams - 1 or j
+ * itself, positions past the length and rows past batch * beams are neither
+ * read for it nor written.
+ *   states   host array of `count` states; different positions and states must
+ *            not overlap (checked where states share a span of memory: WQL_EINVAL)
+ *   parents  device int32 [batch, beams]
+ *   lengths  device int32 [batch], or NULL
+ * beams <= WQL_MAX_BEAMS, batch <= 65535, count <= WQL_MAX_STATES, less than 2^32
+ * bytes in a row of a state, strides below 2^40.  16-byte aligned data and
+ * strides run faster. */
+wql_status wql_beam_reorder(const wql_state* states, int64_t count, const int32_t* parents,
+                            int64_t batch, int64_t beams, const int32_t* lengths,
+                            cudaStream_t stream);
+
 /* Static text for a status code. */
 const char* wql_status_string(wql_status status);
 

@@ -22,6 +22,10 @@ Functions
   wql_mx_logits(x, w, out_dtype, bias=None)         -> logits
   wql_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None)
                                             -> (ids, logp)
+  wql_lora_add(y, x, adapters, ids, out=None)       -> y with the adapters' part
+  wql_beam_select(logits, scores, eos=None, order=BEAM_RANKED)
+                                            -> (tokens, parents, scores, ended)
+  wql_beam_reorder(states, parents, lengths=None, position_dim=None) -> states
   wql_status_string, wql_last_error, wql_launch_count
 """
 from __future__ import annotations
@@ -40,11 +44,14 @@ __all__ = [
     "WQLError", "QuantizedWeight", "Workspace", "load", "wql_quantize", "wql_pack",
     "wql_unpack", "wql_workspace_size", "wql_logits", "wql_logits_noalloc", "wql_topk_rescore",
     "wql_embed_gather", "MXMatrix", "wql_mx_scale_bytes", "wql_mx_quantize", "wql_mx_dequantize",
-    "wql_mx_logits", "wql_add_rmsnorm", "wql_sample", "wql_debug_set_waits",
+    "wql_mx_logits", "wql_add_rmsnorm", "wql_sample", "LoraAdapters", "wql_lora_workspace_size",
+    "wql_lora_add", "wql_beam_workspace_size", "wql_beam_select", "wql_beam_reorder",
+    "wql_debug_set_waits",
     "wql_status_string", "wql_last_error", "wql_launch_count", "F32", "F16", "BF16",
     "CLIP_RTN", "CLIP_MSE", "MAX_TOPK", "NOALLOC_SCRATCH_BYTES", "FMT_SYM", "FMT_E4M3",
     "FMT_ASYM", "MX_FP4", "MX_FP8", "NORM_SAME", "NORM_E4M3", "NORM_MX_FP8", "NORM_MX_FP4",
-    "SAMPLE_MAX_N",
+    "SAMPLE_MAX_N", "LORA_MAX_RANK", "BEAM_RANKED", "BEAM_ANCHORED", "MAX_BEAMS", "BEAM_MAX_N",
+    "MAX_STATES",
 ]
 
 F32, F16, BF16 = 0, 1, 2
@@ -54,6 +61,12 @@ WEIGHT_STATIC = 0x100                    # flag ORed into the format field
 MX_FP4, MX_FP8 = 0, 1                    # wql_mx_format
 NORM_SAME, NORM_E4M3, NORM_MX_FP8, NORM_MX_FP4 = 0, 1, 2, 3    # wql_norm_out
 SAMPLE_MAX_N = 1 << 20
+LORA_MAX_RANK = 128
+LORA_MAX_COUNT = 1 << 22
+BEAM_RANKED, BEAM_ANCHORED = 0, 1        # wql_beam_order
+MAX_BEAMS = 32
+BEAM_MAX_N = 1 << 20
+MAX_STATES = 1024
 MAX_TOPK = 16
 MAX_CTAS = 1024
 _DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -88,6 +101,19 @@ class _WqlMx(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _WqlLora(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("count", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class _WqlState(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("outer", ctypes.c_int64), ("outer_stride", ctypes.c_int64),
+                ("positions", ctypes.c_int64), ("position_stride", ctypes.c_int64),
+                ("position_bytes", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -143,6 +169,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                         vp, vp]
         lib.wql_sample.restype = i32
         lib.wql_sample.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.wql_lora_workspace_size.restype = sz
+        lib.wql_lora_workspace_size.argtypes = [i64, i32]
+        lib.wql_lora_add.restype = i32
+        lib.wql_lora_add.argtypes = [ctypes.POINTER(_WqlLora), vp, i64, vp, vp, vp, vp, sz, vp]
+        lib.wql_beam_workspace_size.restype = sz
+        lib.wql_beam_workspace_size.argtypes = [i64, i64, i64]
+        lib.wql_beam_select.restype = i32
+        lib.wql_beam_select.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp, vp, vp,
+                                        sz, vp]
+        lib.wql_beam_reorder.restype = i32
+        lib.wql_beam_reorder.argtypes = [ctypes.POINTER(_WqlState), i64, vp, i64, i64, vp, vp]
         lib.wql_status_string.restype = ctypes.c_char_p
         lib.wql_status_string.argtypes = [i32]
         lib.wql_last_error.restype = ctypes.c_char_p
@@ -541,3 +578,52 @@ def wql_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor 
     per row (see wql.h).  A row without a logit above -inf gives (-1, NaN), one
     whose logits a bounded wait did not see arrive (-2, NaN)."""
     return (_native or _binding()).sample(logits, u, temperature, top_k, top_p, min_p)
+
+
+@dataclass
+class LoraAdapters:
+    """Low-rank adapters of one projection [n, k], in the layout wql.h documents
+    (wql_lora); smaller ranks are padded with zeros."""
+    a: torch.Tensor                       # [count, rank, k], x's dtype
+    b: torch.Tensor                       # [count, n, rank]
+    scale: torch.Tensor | None = None     # float32 [count]; None: 1
+
+
+def wql_lora_workspace_size(m: int, rank: int) -> int:
+    return int(load().wql_lora_workspace_size(m, rank))
+
+
+def wql_lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor,
+                 out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [*, n], the result of a projection of x [*, k], plus what the adapter
+    ids[row] (int32, one per row; outside the adapters: none) adds to it (see
+    wql.h).  out may be y."""
+    t = (_native or _binding()).lora_add(y, x, adapters.a, adapters.b, adapters.scale, ids, out,
+                                         workspace)
+    return t if out is None else out
+
+
+def wql_beam_workspace_size(batch: int, beams: int, n: int) -> int:
+    return int(load().wql_beam_workspace_size(batch, beams, n))
+
+
+def wql_beam_select(logits: torch.Tensor, scores: torch.Tensor, eos: int | None = None,
+                    order: int = BEAM_RANKED, workspace: torch.Tensor | None = None):
+    """(tokens int32, parents int32, scores, ended), each [batch, beams]: the best
+    continuations of the beams with scores [batch, beams] by the tokens of
+    logits [batch, beams, n] (or [batch * beams, n]), their new scores, and the
+    scores of the beams that end with `eos` now (-inf elsewhere; None without
+    eos).  See wql.h."""
+    return (_native or _binding()).beam_select(logits, scores, eos, order, workspace)
+
+
+def wql_beam_reorder(states, parents: torch.Tensor, lengths: torch.Tensor | None = None,
+                     position_dim: int | None = None):
+    """The states (tensors whose first dimension is batch * beams rows, or more)
+    with their rows moved to where parents [batch, beams] wants them, in place
+    (see wql.h).  With lengths (int32 [batch]) only the first lengths[b] of
+    dimension position_dim move; the dimensions behind it are contiguous."""
+    states = list(states)
+    (_native or _binding()).beam_reorder(states, parents, lengths, position_dim)
+    return states

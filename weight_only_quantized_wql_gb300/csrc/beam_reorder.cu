@@ -1,0 +1,221 @@
+// beam_reorder.cu -- the states of beams follow a selection, in place: row
+// b * beams + j of every state becomes what row b * beams + parents[b, j] was.
+//
+// HBM-bound: what has to move is one read of every parent of a moved beam and
+// one write of every moved beam.  A thread takes the same few bytes of all rows
+// of a sequence: it loads them from the parents and then stores them, and no
+// other thread touches these bytes, so no copy of a state and no barrier is
+// needed.  A parent with several children is read once per child, all but the
+// first time from the L1.
+#include <algorithm>
+
+#include "requests.cuh"
+
+namespace wql {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStates = 64;              // of one launch (4 KB of arguments)
+
+struct States {
+  wql_state s[kStates];
+};
+
+template <typename V> struct Zero;
+template <> struct Zero<uint4> { static __device__ __forceinline__ uint4 get() { return make_uint4(0u, 0u, 0u, 0u); } };
+template <> struct Zero<uint32_t> { static __device__ __forceinline__ uint32_t get() { return 0u; } };
+template <> struct Zero<uint8_t> { static __device__ __forceinline__ uint8_t get() { return 0; } };
+
+// Moves one V of all rows of a sequence at `at`.
+template <typename V, int BEAMS>
+__device__ __forceinline__ void move(unsigned char* at, int64_t row_stride, const int* parent,
+                                     int beams) {
+  V v[BEAMS];
+#pragma unroll
+  for (int j = 0; j < BEAMS; ++j) {
+    v[j] = Zero<V>::get();
+    if (j < beams && parent[j] != j)
+      v[j] = *reinterpret_cast<const V*>(at + parent[j] * row_stride);
+  }
+#pragma unroll
+  for (int j = 0; j < BEAMS; ++j)
+    if (j < beams && parent[j] != j) *reinterpret_cast<V*>(at + j * row_stride) = v[j];
+}
+
+// grid: (tiles, sequences, states).  A run is a piece of a row without gaps:
+// a block's positions where they touch, else one position.  Runs are cut into
+// pieces of sizeof(V) bytes, the last one of a run moved in parts.
+template <typename V, int BEAMS>
+__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const States states,
+                                                                const int32_t* parents, int beams,
+                                                                const int32_t* lengths) {
+  __shared__ int parent[BEAMS];
+  __shared__ int moved;
+  griddep_launch_dependents();
+  griddep_wait();
+  const wql_state& s = states.s[blockIdx.z];
+  const int b = blockIdx.y;
+  if (threadIdx.x == 0) moved = 0;
+  __syncthreads();
+  if (threadIdx.x < beams) {
+    int p = parents[(size_t)b * beams + threadIdx.x];
+    if ((uint32_t)p >= (uint32_t)beams) p = threadIdx.x;
+    parent[threadIdx.x] = p;
+    if (p != (int)threadIdx.x) moved = 1;
+  }
+  __syncthreads();
+  if (!moved) return;
+  int64_t length = s.positions;
+  if (lengths) length = min(length, (int64_t)max(lengths[b], 0));
+  const bool dense = s.position_stride == s.position_bytes;
+  const int64_t run_bytes = dense ? length * s.position_bytes : s.position_bytes;
+  const int64_t inner = dense ? 1 : length;                 // runs of a block
+  const uint32_t pieces = (uint32_t)((run_bytes + sizeof(V) - 1) / sizeof(V));
+  const uint64_t total = (uint64_t)s.outer * inner * pieces;  // below 2^32: bytes of a row
+  unsigned char* data = static_cast<unsigned char*>(s.data) + (int64_t)b * beams * s.row_stride;
+  for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
+       i += (uint64_t)gridDim.x * kThreads) {
+    const uint32_t run = (uint32_t)i / pieces, piece = (uint32_t)i - run * pieces;
+    uint32_t o = run, p = 0;
+    if (!dense) {
+      o = run / (uint32_t)length;
+      p = run - o * (uint32_t)length;
+    }
+    const int64_t in_run = (int64_t)piece * (int64_t)sizeof(V);
+    unsigned char* at = data + o * s.outer_stride + p * s.position_stride + in_run;
+    if (in_run + (int64_t)sizeof(V) <= run_bytes) {
+      move<V, BEAMS>(at, s.row_stride, parent, beams);
+    } else {
+      for (int64_t k = in_run; k < run_bytes; ++k, ++at)
+        move<uint8_t, BEAMS>(at, s.row_stride, parent, beams);
+    }
+  }
+}
+
+template <typename V, int BEAMS>
+cudaError_t launch(const States& st, int count, int64_t largest, const int32_t* parents, int batch,
+                   int beams, const int32_t* lengths, cudaStream_t s) {
+  // enough blocks for several waves, no more than the largest row has tiles
+  const int64_t tiles = (largest + kThreads * (int64_t)sizeof(V) - 1) / (kThreads * (int64_t)sizeof(V));
+  const int64_t want = (64ll * device_sm_count() + (int64_t)batch * count - 1) / ((int64_t)batch * count);
+  const int64_t x = tiles < 1 ? 1 : tiles < want ? tiles : want;
+  const cudaError_t e = launch_pdl(beam_reorder_kernel<V, BEAMS>, dim3((unsigned)x, (unsigned)batch, (unsigned)count),
+                                   dim3(kThreads), 0, s, st, parents, beams, lengths);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+template <typename V>
+cudaError_t launch_b(const States& st, int count, int64_t largest, const int32_t* parents, int batch,
+                     int beams, const int32_t* lengths, cudaStream_t s) {
+  if (beams <= 4) return launch<V, 4>(st, count, largest, parents, batch, beams, lengths, s);
+  if (beams <= 8) return launch<V, 8>(st, count, largest, parents, batch, beams, lengths, s);
+  if (beams <= 16) return launch<V, 16>(st, count, largest, parents, batch, beams, lengths, s);
+  return launch<V, 32>(st, count, largest, parents, batch, beams, lengths, s);
+}
+
+// The widest access that a state's addresses allow.
+int width_of(const wql_state& s) {
+  const bool dense = s.position_stride == s.position_bytes;
+  const uint64_t bits = reinterpret_cast<uintptr_t>(s.data) | (uint64_t)s.row_stride |
+                        (s.outer > 1 ? (uint64_t)s.outer_stride : 0) |
+                        (dense ? 0 : (uint64_t)s.position_stride);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+}
+
+}  // namespace
+
+cudaError_t launch_beam_reorder(const wql_state* states, int64_t count, const int32_t* parents,
+                                int batch, int beams, const int32_t* lengths, cudaStream_t s) {
+  for (const int width : {16, 4, 1}) {
+    States st;
+    int have = 0;
+    int64_t largest = 0;
+    for (int64_t i = 0; i < count; ++i) {
+      const wql_state& w = states[i];
+      const int64_t bytes = w.outer * w.positions * w.position_bytes;
+      if (bytes > 0 && width_of(w) == width) {
+        st.s[have++] = w;
+        if (bytes > largest) largest = bytes;
+      }
+      if (have == kStates || (i + 1 == count && have > 0)) {
+        const cudaError_t e =
+            width == 16 ? launch_b<uint4>(st, have, largest, parents, batch, beams, lengths, s)
+            : width == 4 ? launch_b<uint32_t>(st, have, largest, parents, batch, beams, lengths, s)
+                         : launch_b<uint8_t>(st, have, largest, parents, batch, beams, lengths, s);
+        if (e != cudaSuccess) return e;
+        have = 0;
+        largest = 0;
+      }
+    }
+  }
+  return cudaSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// Overlap, on the host.  Inside a state rows, blocks and positions are nested
+// in some order of their strides; each must hold what is inside it.  Two states
+// whose spans meet must have the same stride at every level that repeats, and
+// at one of them lie apart between its repetitions.
+// ---------------------------------------------------------------------------
+namespace {
+
+struct Level {
+  int64_t count, stride;
+};
+struct Shape {
+  uintptr_t at;
+  Level level[3];                        // largest stride first, those that repeat
+  int levels;
+  int64_t inner;                         // bytes without gaps
+  int64_t extent[4];                     // of one element of level i (extent[levels] = inner)
+};
+
+// False where a state overlaps itself.
+bool shape_of(const wql_state& s, int64_t rows, Shape* out) {
+  Level all[3] = {{rows, s.row_stride}, {s.outer, s.outer_stride}, {s.positions, s.position_stride}};
+  out->at = reinterpret_cast<uintptr_t>(s.data);
+  out->levels = 0;
+  for (const Level& l : all)
+    if (l.count > 1) out->level[out->levels++] = l;
+  for (int i = 0; i < out->levels; ++i)
+    for (int j = i + 1; j < out->levels; ++j)
+      if (out->level[j].stride > out->level[i].stride) std::swap(out->level[i], out->level[j]);
+  out->inner = s.position_bytes;
+  int64_t size = s.position_bytes;
+  for (int i = out->levels - 1; i >= 0; --i) {
+    out->extent[i + 1] = size;
+    if (out->level[i].stride < size) return false;
+    size = (out->level[i].count - 1) * out->level[i].stride + size;
+  }
+  out->extent[0] = size;
+  return true;
+}
+
+// Whether elements of level i share bytes, b's starting d behind a's.
+bool meet(const Shape& a, const Shape& b, int i, int64_t d) {
+  if (d >= a.extent[i] || -d >= b.extent[i]) return false;
+  if (i == a.levels || i == b.levels || a.level[i].stride != b.level[i].stride) return true;
+  const int64_t stride = a.level[i].stride;
+  const int64_t r = ((d % stride) + stride) % stride;
+  // (an element is no larger than the stride: these are its neighbours)
+  return meet(a, b, i + 1, r) || meet(a, b, i + 1, r - stride);
+}
+
+}  // namespace
+
+bool states_overlap(const wql_state* states, int64_t count, int64_t rows) {
+  Shape shapes[WQL_MAX_STATES];
+  int have = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (states[i].outer * states[i].positions * states[i].position_bytes == 0) continue;
+    if (!shape_of(states[i], rows, &shapes[have++])) return true;
+  }
+  std::sort(shapes, shapes + have, [](const Shape& x, const Shape& y) { return x.at < y.at; });
+  for (int i = 0; i < have; ++i)
+    for (int j = i + 1; j < have && shapes[j].at - shapes[i].at < (uintptr_t)shapes[i].extent[0]; ++j)
+      if (meet(shapes[i], shapes[j], 0, (int64_t)(shapes[j].at - shapes[i].at))) return true;
+  return false;
+}
+
+}  // namespace wql

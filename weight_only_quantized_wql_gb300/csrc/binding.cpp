@@ -10,6 +10,7 @@
 #include <optional>
 #include <string>
 #include <tuple>
+#include <vector>
 
 #include "wql.h"
 
@@ -209,6 +210,168 @@ std::tuple<Tensor, Tensor> sample(const Tensor& logits, const Tensor& u,
   return {ids, logp};
 }
 
+// A workspace of this call: torch's allocator orders its reuse on the stream,
+// and a captured call's lies in its graph's own pool.
+Tensor scratch(const MaybeTensor& given, size_t bytes, const Tensor& like) {
+  if (!given) return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+  check_cuda(*given, "workspace");
+  if (given->scalar_type() != at::kByte || given->get_device() != like.get_device())
+    refuse("workspace must hold bytes on cuda:" + std::to_string(like.get_device()));
+  return *given;
+}
+
+Tensor lora_add(const Tensor& y, const Tensor& x, const Tensor& a, const Tensor& b,
+                const MaybeTensor& scale, const Tensor& ids, const MaybeTensor& out,
+                const MaybeTensor& workspace) {
+  const auto [m, k] = rows_of(x, "x");
+  const at::ScalarType type = x.scalar_type();
+  check_cuda(a, "a");
+  check_cuda(b, "b");
+  if (a.dim() != 3 || b.dim() != 3 || a.size(0) != b.size(0) || a.size(1) != b.size(2))
+    refuse("the adapters' a must be [count, rank, k] and b [count, n, rank]");
+  if (a.size(2) != k) refuse("x and the adapters' a must have the same last dimension");
+  if (a.scalar_type() != type || b.scalar_type() != type || a.get_device() != x.get_device() ||
+      b.get_device() != x.get_device())
+    refuse("the adapters must have x's type and lie on its device");
+  const int64_t count = a.size(0), rank = a.size(1), n = b.size(1);
+  if (scale) check_like(*scale, "scale", x, at::kFloat, count);
+  check_like(ids, "ids", x, at::kInt, m);
+  check_like(y, "y", x, type, m * n);
+  if (y.dim() < 1 || y.size(-1) != n) refuse("y's last dimension must be the adapters' n");
+  if (out) check_like(*out, "out", x, type, m * n);
+  const c10::cuda::CUDAGuard on(x.device());
+  Tensor to = out ? *out : at::empty_like(y);
+  const Tensor ws = scratch(workspace, wql_lora_workspace_size(m, (int32_t)rank), x);
+  const wql_lora w{dtype_code(type), (int32_t)rank, count, n, k, a.const_data_ptr(),
+                   b.const_data_ptr(), static_cast<const float*>(pointer(scale))};
+  check_status("wql_lora_add",
+               wql_lora_add(&w, x.const_data_ptr(), m, static_cast<const int32_t*>(ids.const_data_ptr()),
+                            y.const_data_ptr(), to.data_ptr(), ws.data_ptr(), (size_t)ws.numel(),
+                            stream_of(x)));
+  return to;
+}
+
+// (tokens, parents, scores, ended)
+std::tuple<Tensor, Tensor, Tensor, MaybeTensor> beam_select(const Tensor& logits,
+                                                            const Tensor& scores,
+                                                            std::optional<int64_t> eos,
+                                                            int64_t order,
+                                                            const MaybeTensor& workspace) {
+  const auto [rows, n] = rows_of(logits, "logits");
+  if (scores.dim() != 2) refuse("scores must be [batch, beams]");
+  check_like(scores, "scores", logits, at::kFloat, rows);
+  const int64_t batch = scores.size(0), beams = scores.size(1);
+  if (eos && (*eos < 0 || *eos >= n)) refuse("eos must be a token of the vocabulary, or None");
+  if (order != WQL_BEAM_RANKED && order != WQL_BEAM_ANCHORED)
+    refuse("order must be BEAM_RANKED or BEAM_ANCHORED");
+  const c10::cuda::CUDAGuard on(logits.device());
+  Tensor tokens = at::empty({batch, beams}, logits.options().dtype(at::kInt));
+  Tensor parents = at::empty_like(tokens);
+  Tensor best = at::empty_like(scores);
+  MaybeTensor ended;
+  if (eos) ended = at::empty_like(scores);
+  const Tensor ws = scratch(workspace, wql_beam_workspace_size(batch, beams, n), logits);
+  check_status(
+      "wql_beam_select",
+      wql_beam_select(logits.const_data_ptr(), dtype_code(logits.scalar_type()), batch, beams, n,
+                      static_cast<const float*>(scores.const_data_ptr()),
+                      eos ? (int32_t)*eos : -1, (int32_t)order,
+                      static_cast<int32_t*>(tokens.data_ptr()),
+                      static_cast<int32_t*>(parents.data_ptr()),
+                      static_cast<float*>(best.data_ptr()),
+                      ended ? static_cast<float*>(ended->data_ptr()) : nullptr, ws.data_ptr(),
+                      (size_t)ws.numel(), stream_of(logits)));
+  return {tokens, parents, best, ended};
+}
+
+// The dimensions [from, to) of a tensor as one, given what lies behind them.
+struct Folded {
+  int64_t count = 1, stride = 0;         // bytes
+};
+bool fold(const Tensor& t, int64_t from, int64_t to, Folded* f) {
+  const int64_t size = t.element_size();
+  for (int64_t d = to - 1; d >= from; --d) {
+    if (t.size(d) == 1) continue;
+    const int64_t stride = t.stride(d) * size;
+    if (f->count == 1) f->stride = stride;
+    else if (stride != f->stride * f->count) return false;
+    f->count *= t.size(d);
+  }
+  return true;
+}
+
+wql_state state_of(Tensor& t, int64_t rows, const std::optional<int64_t>& position_dim) {
+  if (!t.is_cuda()) refuse("states must be CUDA tensors (the library has no CPU path)");
+  if (t.dim() < 1 || t.size(0) < rows)
+    refuse("a state's first dimension must hold batch * beams = " + std::to_string(rows) + " rows");
+  const int64_t size = t.element_size(), dims = t.dim();
+  wql_state s{};
+  s.data = t.data_ptr();
+  s.row_stride = t.stride(0) * size;
+  s.outer = s.positions = 1;
+  if (t.numel() == 0) {
+    s.positions = 0;
+    return s;
+  }
+  // what is contiguous at the end
+  int64_t inner = dims;
+  const int64_t stop = position_dim ? *position_dim + 1 : 1;
+  s.position_bytes = size;
+  while (inner > stop && (t.size(inner - 1) == 1 || t.stride(inner - 1) * size == s.position_bytes)) {
+    --inner;
+    s.position_bytes *= t.size(inner);
+  }
+  Folded positions, outer;
+  if (position_dim) {
+    if (inner != stop) refuse("the dimensions behind position_dim must be contiguous");
+    fold(t, *position_dim, stop, &positions);
+    if (!fold(t, 1, *position_dim, &outer))
+      refuse("the dimensions between the rows and position_dim must have a common stride");
+  } else {
+    // up to two levels of gaps
+    int64_t d = inner;
+    while (d > 1) {
+      Folded next = positions;
+      if (!fold(t, d - 1, d, &next)) break;
+      positions = next;
+      --d;
+    }
+    if (!fold(t, 1, d, &outer)) refuse("a state's strides must fall into at most two levels of gaps");
+  }
+  s.positions = positions.count;
+  s.position_stride = positions.count > 1 ? positions.stride : s.position_bytes;
+  s.outer = outer.count;
+  s.outer_stride = outer.stride;
+  return s;
+}
+
+void beam_reorder(std::vector<Tensor>& states, const Tensor& parents, const MaybeTensor& lengths,
+                  const std::optional<int64_t>& position_dim) {
+  if (states.empty()) return;
+  if (parents.dim() != 2) refuse("parents must be [batch, beams]");
+  const int64_t batch = parents.size(0), beams = parents.size(1);
+  const Tensor& first = states[0];
+  if (!first.is_cuda()) refuse("states must be CUDA tensors (the library has no CPU path)");
+  check_like(parents, "parents", first, at::kInt, batch * beams);
+  if (lengths) {
+    if (!position_dim) refuse("lengths need position_dim");
+    check_like(*lengths, "lengths", first, at::kInt, batch);
+  }
+  std::vector<wql_state> list;
+  list.reserve(states.size());
+  for (Tensor& t : states) {
+    if (t.get_device() != first.get_device()) refuse("states must lie on one device");
+    if (position_dim && (*position_dim < 1 || *position_dim >= t.dim()))
+      refuse("position_dim must be a dimension of every state behind the rows");
+    list.push_back(state_of(t, batch * beams, position_dim));
+  }
+  const c10::cuda::CUDAGuard on(first.device());
+  check_status("wql_beam_reorder",
+               wql_beam_reorder(list.data(), (int64_t)list.size(),
+                                static_cast<const int32_t*>(parents.const_data_ptr()), batch, beams,
+                                static_cast<const int32_t*>(pointer(lengths)), stream_of(first)));
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_wql_torch, m) {
@@ -217,4 +380,7 @@ PYBIND11_MODULE(_wql_torch, m) {
   m.def("mx_logits", &mx_logits);
   m.def("add_rmsnorm", &add_rmsnorm);
   m.def("sample", &sample);
+  m.def("lora_add", &lora_add);
+  m.def("beam_select", &beam_select);
+  m.def("beam_reorder", &beam_reorder);
 }

@@ -16,6 +16,7 @@
 #include "wql_common.cuh"
 #include "embed.cuh"
 #include "mx.cuh"
+#include "requests.cuh"
 
 namespace wql {
 
@@ -73,6 +74,8 @@ namespace {
 std::atomic<uint64_t> g_launches{0};
 thread_local std::string g_last_error;
 constexpr int kDecodeMaxTokens = 16;
+constexpr int64_t kLoraMaxTokens = int64_t(1) << 23;   // 2^15 slices of 256
+constexpr int64_t kBeamMaxRows = int64_t(1) << 20;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool half_dtype(int d) { return d == WQL_F16 || d == WQL_BF16; }
@@ -569,6 +572,127 @@ wql_status wql_sample(const void* logits, int32_t dtype, int64_t m, int64_t n, c
   a.wait_budget = diag_wait_budget();
   a.diag_stall = diag_stall_mma();
   const cudaError_t e = launch_sample(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+size_t wql_lora_workspace_size(int64_t m, int32_t rank) {
+  if (m <= 0 || m > kLoraMaxTokens || rank <= 0 || rank > WQL_LORA_MAX_RANK) return 0;
+  return round_up((size_t)m * lora_chunks(rank) * 64, 256) + round_up((size_t)m * 4, 256);
+}
+
+wql_status wql_lora_add(const wql_lora* w, const void* x, int64_t m, const int32_t* ids,
+                        const void* y, void* out, void* workspace, size_t ws_bytes,
+                        cudaStream_t stream) {
+  if (!w || m < 0 || w->count < 0 || w->n < 0 || w->k <= 0 || w->rank <= 0) return WQL_EINVAL;
+  const bool work = m > 0 && w->n > 0;
+  if (work && (!x || !ids || !y || !out)) return WQL_EINVAL;
+  if (work && w->count > 0 && (!w->a || !w->b)) return WQL_EINVAL;
+  if (!half_dtype(w->dtype) || w->rank % 8 != 0 || w->rank > WQL_LORA_MAX_RANK) return WQL_EUNSUPPORTED;
+  if (w->k % 8 != 0 || w->k > kMxMaxK || w->n >= (int64_t(1) << 31) ||
+      w->count >= WQL_LORA_MAX_COUNT || m > kLoraMaxTokens)
+    return WQL_EUNSUPPORTED;
+  if (!aligned(w->a, 16) || !aligned(w->b, 16) || !aligned(w->scale, 4) || !aligned(x, 16) ||
+      !aligned(ids, 4) || !aligned(y, 2) || !aligned(out, 2))
+    return WQL_EUNSUPPORTED;
+  if (!work) return WQL_OK;
+  const size_t u_bytes = round_up((size_t)m * lora_chunks(w->rank) * 64, 256);
+  if (!workspace || ws_bytes < wql_lora_workspace_size(m, w->rank) || !aligned(workspace, 256))
+    return WQL_EWORKSPACE;
+  LoraArgs a{};
+  a.a = w->a;
+  a.b = w->b;
+  a.scale = w->scale;
+  a.x = x;
+  a.ids = ids;
+  a.y = y;
+  a.out = out;
+  a.u = static_cast<uint4*>(workspace);
+  a.factor = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + u_bytes);
+  a.dtype = w->dtype;
+  a.rank = w->rank;
+  a.chunks = lora_chunks(w->rank);
+  a.count = (int)w->count;
+  a.n = (int)w->n;
+  a.k = (int)w->k;
+  a.m = (int)m;
+  const cudaError_t e = launch_lora_add(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n) {
+  if (batch <= 0 || beams <= 0 || beams > WQL_MAX_BEAMS || n <= 0 || n > WQL_BEAM_MAX_N ||
+      batch > kBeamMaxRows / beams)
+    return 0;
+  const size_t parts = (size_t)batch * beams * beam_parts(batch * beams, n);
+  return round_up(parts * sizeof(float2), 256) + round_up(parts * beams * 8, 256);
+}
+
+wql_status wql_beam_select(const void* logits, int32_t dtype, int64_t batch, int64_t beams,
+                           int64_t n, const float* scores, int32_t eos, int32_t order,
+                           int32_t* tokens_out, int32_t* parents_out, float* scores_out,
+                           float* ended_out, void* workspace, size_t ws_bytes,
+                           cudaStream_t stream) {
+  if (batch < 0 || beams <= 0 || n <= 0 || eos < -1 || eos >= n) return WQL_EINVAL;
+  if (order != WQL_BEAM_RANKED && order != WQL_BEAM_ANCHORED) return WQL_EINVAL;
+  if (batch > 0 && (!logits || !scores || !tokens_out || !parents_out || !scores_out))
+    return WQL_EINVAL;
+  if (dtype != WQL_F32 && !half_dtype(dtype)) return WQL_EUNSUPPORTED;
+  if (beams > WQL_MAX_BEAMS || n > WQL_BEAM_MAX_N || batch > kBeamMaxRows / beams)
+    return WQL_EUNSUPPORTED;
+  if (!aligned(logits, dtype == WQL_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(tokens_out, 4) ||
+      !aligned(parents_out, 4) || !aligned(scores_out, 4) || !aligned(ended_out, 4))
+    return WQL_EUNSUPPORTED;
+  if (batch == 0) return WQL_OK;
+  if (!workspace || ws_bytes < wql_beam_workspace_size(batch, beams, n) || !aligned(workspace, 256))
+    return WQL_EWORKSPACE;
+  BeamSelectArgs a{};
+  a.logits = logits;
+  a.dtype = dtype;
+  a.batch = (int)batch;
+  a.beams = (int)beams;
+  a.n = (int)n;
+  a.eos = eos;
+  a.order = order;
+  a.scores = scores;
+  a.tokens = tokens_out;
+  a.parents = parents_out;
+  a.scores_out = scores_out;
+  a.ended = ended_out;
+  a.parts = beam_parts(batch * beams, n);
+  a.stats = static_cast<float2*>(workspace);
+  a.keys = reinterpret_cast<uint64_t*>(
+      static_cast<unsigned char*>(workspace) +
+      round_up((size_t)batch * beams * a.parts * sizeof(float2), 256));
+  const cudaError_t e = launch_beam_select(a, stream);
+  return e == cudaSuccess ? WQL_OK : cuda_fail(e);
+}
+
+wql_status wql_beam_reorder(const wql_state* states, int64_t count, const int32_t* parents,
+                            int64_t batch, int64_t beams, const int32_t* lengths,
+                            cudaStream_t stream) {
+  if (count < 0 || batch < 0 || beams <= 0) return WQL_EINVAL;
+  if ((count > 0 && !states) || (count > 0 && batch > 0 && !parents)) return WQL_EINVAL;
+  if (beams > WQL_MAX_BEAMS || batch > 65535 || count > WQL_MAX_STATES) return WQL_EUNSUPPORTED;
+  if (!aligned(parents, 4) || !aligned(lengths, 4)) return WQL_EUNSUPPORTED;
+  constexpr int64_t kMaxStride = int64_t(1) << 40, kMaxBytes = (int64_t(1) << 32) - 1;
+  for (int64_t i = 0; i < count; ++i) {
+    const wql_state& s = states[i];
+    if (s.outer < 0 || s.positions < 0 || s.position_bytes < 0 || s.row_stride < 0 ||
+        s.outer_stride < 0 || s.position_stride < 0)
+      return WQL_EINVAL;
+    const bool empty = s.outer == 0 || s.positions == 0 || s.position_bytes == 0 || batch == 0;
+    if (!empty && !s.data) return WQL_EINVAL;
+    if (s.row_stride >= kMaxStride || s.outer_stride >= kMaxStride || s.position_stride >= kMaxStride)
+      return WQL_EUNSUPPORTED;
+    if (!empty && (s.outer > kMaxBytes / s.positions ||
+                   s.outer * s.positions > kMaxBytes / s.position_bytes))
+      return WQL_EUNSUPPORTED;
+  }
+  if (count == 0 || batch == 0) return WQL_OK;
+  if (states_overlap(states, count, batch * beams)) return WQL_EINVAL;
+  if (beams == 1) return WQL_OK;
+  const cudaError_t e = launch_beam_reorder(states, count, parents, (int)batch, (int)beams, lengths,
+                                            stream);
   return e == cudaSuccess ? WQL_OK : cuda_fail(e);
 }
 
