@@ -67,7 +67,7 @@ def check_lora(got, y, x, a, b, scale, ids, dt):
 LORA = [(1, 1, 8, 8, 1), (1, 1000, 64, 16, 3), (1, 999, 5120, 16, 2), (5, 777, 72, 24, 2),
         (16, 128, 512, 32, 1), (17, 64, 40, 32, 1), (33, 1003, 136, 8, 5), (40, 264, 1032, 56, 40),
         (300, 520, 256, 64, 7), (257, 97, 1024, 128, 3), (9, 2056, 5120, 40, 9),
-        (520, 72, 96, 104, 2)]
+        (520, 72, 96, 104, 2), (530, 72, 200, 24, 3), (513, 40, 136, 64, 9), (700, 80, 5120, 16, 20)]
 
 
 @pytest.mark.parametrize("m,n,k,r,count", LORA)

@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "requests.cuh"
+#include "sm100.cuh"
 
 namespace wql {
 namespace {
@@ -92,15 +93,130 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const States sta
   }
 }
 
+// The same for 16-byte pieces of up to kAsyncBeams rows, without registers for
+// what is under way: a thread's pieces of the parents go to its own places in
+// shared memory, kStages columns ahead, and from there to the children.
+constexpr int kAsyncBeams = 16;
+constexpr int kStages = 3;
+
+__global__ void __launch_bounds__(kThreads) beam_reorder_async_kernel(const States states,
+                                                                      const int32_t* parents, int beams,
+                                                                      const int32_t* lengths) {
+  extern __shared__ uint4 ring[];              // [stage][beam][thread]
+  __shared__ int parent[kAsyncBeams];
+  griddep_launch_dependents();
+  griddep_wait();
+  const wql_state& s = states.s[blockIdx.z];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  // every warp for itself: the rows that are written, and those that are read
+  int p = lane < beams ? parents[(size_t)b * beams + lane] : -1;
+  const bool moves = (uint32_t)p < (uint32_t)beams && p != lane;
+  if (tid < beams) parent[tid] = p;
+  const uint32_t children = __ballot_sync(0xFFFFFFFFu, moves);
+  const uint32_t read = __reduce_or_sync(0xFFFFFFFFu, moves ? 1u << p : 0u);
+  __syncthreads();
+  if (children == 0u) return;
+  int64_t length = s.positions;
+  if (lengths) length = min(length, (int64_t)max(lengths[b], 0));
+  const bool dense = s.position_stride == s.position_bytes;
+  const int64_t run_bytes = dense ? length * s.position_bytes : s.position_bytes;
+  const uint32_t pieces = (uint32_t)((run_bytes + 15) / 16);
+  const uint64_t total = (uint64_t)s.outer * (dense ? 1 : length) * pieces;    // below 2^32
+  unsigned char* data = static_cast<unsigned char*>(s.data) + (int64_t)b * beams * s.row_stride;
+  const uint64_t step = (uint64_t)gridDim.x * kThreads;
+  uint64_t i = (uint64_t)blockIdx.x * kThreads + tid;
+
+  struct Piece {
+    unsigned char* at;                         // in row 0; null: none
+    int bytes;
+  };
+  auto piece_at = [&](uint64_t k) {
+    if (k >= total) return Piece{nullptr, 0};
+    const uint32_t run = (uint32_t)k / pieces, piece = (uint32_t)k - run * pieces;
+    uint32_t o = run, q = 0;
+    if (!dense) {
+      o = run / (uint32_t)length;
+      q = run - o * (uint32_t)length;
+    }
+    const int64_t in_run = (int64_t)piece * 16;
+    return Piece{data + o * s.outer_stride + q * s.position_stride + in_run,
+                 (int)min((int64_t)16, run_bytes - in_run)};
+  };
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + tid * 16;
+  const uint32_t stage_bytes = (uint32_t)beams * kThreads * 16;
+  auto load = [&](const Piece& w, uint32_t to) {
+    if (w.bytes == 16)
+      for (uint32_t m = read; m != 0u; m &= m - 1u) {
+        const int r = __ffs(m) - 1;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + r * (kThreads * 16)),
+                     "l"(w.at + r * s.row_stride) : "memory");
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto store = [&](const Piece& w, uint32_t from) {
+    if (w.bytes == 16) {
+      for (uint32_t m = children; m != 0u; m &= m - 1u) {
+        const int j = __ffs(m) - 1;
+        *reinterpret_cast<uint4*>(w.at + j * s.row_stride) = lds128(from + parent[j] * (kThreads * 16));
+      }
+    } else {                                   // the end of a run
+      for (int k = 0; k < w.bytes; ++k) {
+        uint8_t v[kAsyncBeams];
+#pragma unroll
+        for (int j = 0; j < kAsyncBeams; ++j)
+          if (children >> j & 1u) v[j] = w.at[k + parent[j] * s.row_stride];
+#pragma unroll
+        for (int j = 0; j < kAsyncBeams; ++j)
+          if (children >> j & 1u) w.at[k + j * s.row_stride] = v[j];
+      }
+    }
+  };
+  Piece queue[kStages];
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) {
+    queue[k] = piece_at(i + k * step);
+    load(queue[k], mine + k * stage_bytes);
+  }
+  while (queue[0].at != nullptr) {
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      store(queue[k], mine + k * stage_bytes);
+      queue[k] = piece_at(i + (kStages + k) * step);
+      load(queue[k], mine + k * stage_bytes);
+    }
+    i += kStages * step;
+  }
+}
+
 template <typename V, int BEAMS>
 cudaError_t launch(const States& st, int count, int64_t largest, const int32_t* parents, int batch,
                    int beams, const int32_t* lengths, cudaStream_t s) {
-  // enough blocks for several waves, no more than the largest row has tiles
+  // Enough blocks for eight waves, no more than the largest row has tiles.  (Of
+  // those with shared memory an SM holds fewer: 9 x 8 beams anchored 60 us with
+  // 8 waves, 84 with 32.)
   const int64_t tiles = (largest + kThreads * (int64_t)sizeof(V) - 1) / (kThreads * (int64_t)sizeof(V));
-  const int64_t want = (64ll * device_sm_count() + (int64_t)batch * count - 1) / ((int64_t)batch * count);
-  const int64_t x = tiles < 1 ? 1 : tiles < want ? tiles : want;
-  const cudaError_t e = launch_pdl(beam_reorder_kernel<V, BEAMS>, dim3((unsigned)x, (unsigned)batch, (unsigned)count),
-                                   dim3(kThreads), 0, s, st, parents, beams, lengths);
+  const size_t smem = (size_t)kStages * beams * kThreads * 16;
+  auto blocks = [&](int64_t resident) {
+    const int64_t want = (8 * resident * device_sm_count() + (int64_t)batch * count - 1) / ((int64_t)batch * count);
+    return dim3((unsigned)(tiles < want ? tiles : want), (unsigned)batch, (unsigned)count);
+  };
+  if constexpr (sizeof(V) == 16) {
+    const int64_t resident = (int64_t)(200 * 1024 / smem) > 0 ? (int64_t)(200 * 1024 / smem) : 1;
+    const dim3 grid = blocks(resident);
+    // a column or two a thread: nothing to copy ahead (one sequence of 4 beams, 48
+    // states of 77 KB a row: 4.2 us by registers, 5.2 through shared memory)
+    if (beams <= kAsyncBeams && tiles > 2 * (int64_t)grid.x) {
+      static LargestPerDevice limit;
+      cudaError_t e = allow_smem(limit, beam_reorder_async_kernel, smem);
+      if (e != cudaSuccess) return e;
+      e = launch_pdl(beam_reorder_async_kernel, grid, dim3(kThreads), smem, s, st, parents, beams, lengths);
+      if (e == cudaSuccess) note_launch();
+      return e;
+    }
+  }
+  const cudaError_t e = launch_pdl(beam_reorder_kernel<V, BEAMS>, blocks(8), dim3(kThreads), 0, s, st, parents,
+                                   beams, lengths);
   if (e == cudaSuccess) note_launch();
   return e;
 }

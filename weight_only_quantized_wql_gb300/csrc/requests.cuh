@@ -13,6 +13,9 @@ namespace wql {
 // Ranks are padded to 16, 32, 64 or 128: chunks of 16, the k of one mma.
 inline int lora_chunks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
+// Tokens are grouped by adapter in slices.
+constexpr int kLoraSlice = 256;
+
 struct LoraArgs {
   const void* a;
   const void* b;
@@ -42,11 +45,13 @@ struct BeamSelectArgs {
   float* ended;               // or null
   float2* stats;              // workspace: [rows][parts]
   uint64_t* keys;             // workspace: [rows][parts][beams]
-  int parts;                  // of a row, beam_parts()
+  int parts, part_chunks;     // beam_parts()
 };
-// Parts of a row, and elements of one.
-int beam_part_elements(int64_t rows, int64_t n);
-int beam_parts(int64_t rows, int64_t n);
+// Parts of a row, and chunks of one.
+struct BeamParts {
+  int parts, chunks;
+};
+BeamParts beam_parts(int64_t rows, int64_t n, int dtype);
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t s);
 
 cudaError_t launch_beam_reorder(const wql_state* states, int64_t count, const int32_t* parents,

@@ -623,7 +623,9 @@ size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n) {
   if (batch <= 0 || beams <= 0 || beams > WQL_MAX_BEAMS || n <= 0 || n > WQL_BEAM_MAX_N ||
       batch > kBeamMaxRows / beams)
     return 0;
-  const size_t parts = (size_t)batch * beams * beam_parts(batch * beams, n);
+  const int wide = beam_parts(batch * beams, n, WQL_F32).parts;
+  const int half = beam_parts(batch * beams, n, WQL_F16).parts;
+  const size_t parts = (size_t)batch * beams * (wide > half ? wide : half);
   return round_up(parts * sizeof(float2), 256) + round_up(parts * beams * 8, 256);
 }
 
@@ -658,7 +660,9 @@ wql_status wql_beam_select(const void* logits, int32_t dtype, int64_t batch, int
   a.parents = parents_out;
   a.scores_out = scores_out;
   a.ended = ended_out;
-  a.parts = beam_parts(batch * beams, n);
+  const BeamParts cut = beam_parts(batch * beams, n, dtype);
+  a.parts = cut.parts;
+  a.part_chunks = cut.chunks;
   a.stats = static_cast<float2*>(workspace);
   a.keys = reinterpret_cast<uint64_t*>(
       static_cast<unsigned char*>(workspace) +
