@@ -112,7 +112,8 @@ def _link_binding(obj: str) -> None:
     # the library beside it is found by name, so that both are one instance
     _link("link of the binding", BINDING,
           ["g++", "-shared", obj, f"-L{BUILD}", "-l:libwql.so", "-Wl,-rpath,$ORIGIN",
-           f"-L{torch_lib}", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda"])
+           f"-L{torch_lib}", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10",
+           "-lc10_cuda"])
     with open(BINDING_FOR, "w") as f:
         f.write(_built_for())
 
