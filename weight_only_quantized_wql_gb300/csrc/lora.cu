@@ -413,21 +413,17 @@ template <int N, typename F> __device__ __forceinline__ void for_each(F f) {
 }
 
 
-// A lane's column (and the 32nd behind it) of a group's rows, two rows in a word.
-template <int UNITS>
-__device__ __forceinline__ void load_columns(const LoraArgs& a, const Sorted& sorted, int base, int p,
-                                             int count, int64_t column, uint32_t (&v)[UNITS][8]) {
-  const unsigned short* y = static_cast<const unsigned short*>(a.y) + column;
+// A lane's column of a group's rows, four rows at a time; no branch waits for
+// what the ones before it load.
+__device__ __forceinline__ void load_column(const LoraArgs& a, const Sorted& sorted, int base, int p,
+                                            int count, int64_t column, uint32_t (&v)[16]) {
+  const unsigned short* y = static_cast<const unsigned short*>(a.y) + min(column, (int64_t)a.n - 1);
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u)
+  for (int j = 0; j < 16; j += 4)
+    if (j < count) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      if (j >= count) break;
-      const bool in = column + 32 * u < a.n;
-      uint32_t q = in ? __ldcg(y + (int64_t)(base + (int)(sorted.key[p + j] & 255u)) * a.n + 32 * u) : 0u;
-      if (j + 1 < count && in)
-        q |= (uint32_t)__ldcg(y + (int64_t)(base + (int)(sorted.key[p + j + 1] & 255u)) * a.n + 32 * u) << 16;
-      v[u][j / 2] = q;
+      for (int i = j; i < j + 4; ++i)          // (past the last row: the last one again)
+        v[i] = __ldcg(y + (int64_t)(base + (int)(sorted.key[p + min(i, count - 1)] & 255u)) * a.n);
     }
 }
 
@@ -552,10 +548,10 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
       ua[c] = u0[4 * c];
       ub[c] = u1[4 * c];
     }
-    // y: WIDE, rows g and g + 8, 8 columns a unit; else a column a lane, two rows
-    // in a word
-    uint32_t y[UNITS][8];
-    if constexpr (!WIDE) load_columns<UNITS>(a, sorted, base, p, count, col0 + lane, y);
+    // y: WIDE, rows g and g + 8, 8 columns a unit; else a column a lane
+    uint32_t y[UNITS][WIDE ? 8 : 16];
+    static_assert(WIDE || UNITS == 1, "a column a lane");
+    if constexpr (!WIDE) load_column(a, sorted, base, p, count, col0 + lane, y[0]);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const char* slot = mine + offset;
@@ -636,13 +632,11 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
             turn[warp][g + 8][8 * t + 2 * j + e] = f1 * acc[j][2 + e];
           }
         __syncwarp();
-        const int column = 32 * u + lane;
-        T* to = static_cast<T*>(a.out) + col0 + column;
+        T* to = static_cast<T*>(a.out) + col0 + lane;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (j >= count) break;
-          const float v = j & 1 ? high<T>(y[u][j / 2]) : low<T>(y[u][j / 2]);
-          if (column < columns) to[(int64_t)token(p + j) * a.n] = from_f32<T>(v + turn[warp][j][lane]);
+          if (lane < columns) to[(int64_t)token(p + j) * a.n] = from_f32<T>(low<T>(y[0][j]) + turn[warp][j][lane]);
         }
       }
     }
@@ -676,7 +670,7 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
 
 template <typename T, int CHUNKS, bool WIDE>
 cudaError_t launch_up(const LoraArgs& a, int groups, int slices, cudaStream_t s) {
-  constexpr int kUnits = CHUNKS == 1 ? 2 : 1;
+  constexpr int kUnits = CHUNKS == 1 && WIDE ? 2 : 1;
   using S = Stage<CHUNKS, kUnits, WIDE>;
   constexpr size_t kRing = (size_t)kUpThreads / 32 * S::kStages * S::kBytes;
   auto kern = lora_up_kernel<T, CHUNKS, kUnits, WIDE>;
