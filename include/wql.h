@@ -484,16 +484,16 @@ size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n);
 /* One step of beam search for `batch` sequences of `beams` beams each.  The
  * continuation of beam w by token v scores
  *   s[w, v] = scores[w] + l[w, v] - log sum_v' exp(l[w, v']),
- * l the logits: exponentials in fp32 over the row's largest logit, sums over a
- * row's parts and scores in binary64, rounded to fp32 at the end.  Of a
- * sequence's beams * n continuations the best `beams` whose token is not `eos`
- * are selected: score descending, then beam ascending, then, within a beam,
- * logit descending and token ascending.
- *   A NaN logit counts as -inf; so does one of -inf give no continuation.  In a
- *   row with logits of +inf those score scores[w] and no other continues.  A beam
- *   whose score is not finite has no continuations.  Where fewer than `beams` are
- *   left, the rest of the slots (the free ones in ascending order) get token -1,
- *   parent -1 and score -inf.
+ * l the logits: exponentials in fp32 and sums of them over parts of a row, the
+ * sums over the parts and the scores in two fp32 parts (some 46 bits), rounded to
+ * fp32 at the end; scores are compared before that.  Of a sequence's beams * n
+ * continuations the best `beams` whose token is not `eos` are selected: score
+ * descending, then beam ascending, then, within a beam, logit descending and
+ * token ascending.
+ *   A logit of -inf, or NaN, gives no continuation.  In a row with logits of +inf
+ *   those score scores[w] and no other continues.  A beam whose score is not finite
+ *   has no continuations.  Where fewer than `beams` are left, the rest of the slots
+ *   (the free ones in ascending order) get token -1, parent -1 and score -inf.
  *   logits       device [batch, beams, n] of dtype (F32, F16 or BF16), aligned to
  *                its elements
  *   scores       device float [batch, beams]: log-probabilities of the beams (for

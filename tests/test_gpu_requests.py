@@ -618,3 +618,20 @@ def test_streams_do_not_disturb_one_another():
     for i in (0, 1):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_example_runs():
+    """examples/beam_step.py, eagerly and as a graph."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "beam_step.py")
+    spec = importlib.util.spec_from_file_location("beam_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    import sys
+    sys.modules["beam_step"] = mod                 # dataclasses look it up
+    spec.loader.exec_module(mod)
+    eager = mod.search(3, 4, 2000, 128, 5, graph=False)
+    graph = mod.search(3, 4, 2000, 128, 5, graph=True)
+    assert all(torch.equal(x, y) for x, y in zip(eager, graph))
+    assert torch.isfinite(eager[1]).all() and eager[0].shape == (3, 4, 5)
+    assert (eager[0] != mod.EOS).all()

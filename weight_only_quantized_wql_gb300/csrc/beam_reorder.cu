@@ -2,11 +2,15 @@
 // b * beams + j of every state becomes what row b * beams + parents[b, j] was.
 //
 // HBM-bound: what has to move is one read of every parent of a moved beam and
-// one write of every moved beam.  A thread takes the same few bytes of all rows
-// of a sequence: it loads them from the parents and then stores them, and no
-// other thread touches these bytes, so no copy of a state and no barrier is
-// needed.  A parent with several children is read once per child, all but the
-// first time from the L1.
+// one write of every moved beam.  A thread takes the same 16 bytes of all rows of
+// a sequence: it loads them from the parents and then stores them to the
+// children, and no other thread touches these bytes, so no copy of a state and no
+// barrier is needed.  Where there is enough to move, the pieces wait in shared
+// memory instead of registers (16 sequences of 4 beams, 32 states: 141 us, 190
+// through registers), which also reads a parent of several children once.
+// Measured: that case, ranked, 88 % of the copy rate; 9 x 8 beams, anchored, 12
+// states of 746 KB a row, 60.5 us (98 %); one sequence of 4 beams, 48 states of 77
+// KB a row, 4.2 us.
 #include <algorithm>
 
 #include "requests.cuh"

@@ -7,8 +7,16 @@
 // the best of each row's lists, and the best of those.
 //
 // Inside a row the order of the scores is that of the logits, so lists hold
-// (logit, token) keys and no score; scores exist for beams * beams keys only.  Every order is total (ties by token, then by beam), hence results
-// do not depend on the order in which lists were filled.
+// (logit, token) keys and no score; scores exist for beams * beams keys only.
+// Every order is total (ties by token, then by beam), hence results do not
+// depend on the order in which lists were filled.
+//
+// HBM-bound, where there are logits enough: 16 sequences x 16 beams x 248320 fp32
+// 53.5 us (70 % of the copy rate), 64 x 4 x 151936 bf16 24.3 us (47 %): its logits
+// arrive in 11 to 14 us, at the copy rate; 3.5 us follow for the ends of the
+// parts, 1 for the second launch and 3 for the joining.  1 x 4 x 151936 bf16 7.7
+// us, 7 x 5 x 50303 fp16 10.0 us, of which the two launches and their dependent
+// steps are all.
 #include "requests.cuh"
 #include "sm100.cuh"
 
@@ -19,10 +27,10 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kResident = 4;             // blocks on an SM
 constexpr int kVecs = 4;                 // 16-byte groups a lane takes of a chunk
-constexpr int kStages = 2;              // chunks on their way to a warp
+constexpr int kStages = 2;               // chunks on their way to a warp
 constexpr int kSlot = 32 * kVecs + 1;    // 16-byte groups of one
 constexpr size_t kRing = (size_t)kWarps * kStages * kSlot * 16;
-constexpr int kBlocks = 152 * kResident;        // at a time on 152 SMs
+constexpr int kBlocks = 152 * kResident; // at a time on 152 SMs
 constexpr int kTops = 16;                // chunks whose maxima are held
 constexpr int kList = 64;                // a warp's list: the best and 32 more
 constexpr int kStaged = 4096;            // keys of a sequence that are joined in shared memory
@@ -223,8 +231,11 @@ struct Best {
 // to the warps in turn and copied ahead into each warp's own ring.  Every lane
 // keeps its own maximum and sum, and the maximum of its group of each chunk.
 // The loop over the logits looks for nothing else: at its end the beams-th
-// largest of the maxima of 32 columns of lanes bounds the best continuations from
-// below, and the few groups that reach it are read once more.
+// largest of the maxima of 64 columns of lanes bounds the best continuations from
+// below, and the few groups that reach it are read once more.  (Appending to
+// lists inside the loop cost more than the sums: 64 x 4 x 151936 bf16 44 us for
+// the call.)  Blocks stay and take a part after another; their copies run on into
+// the next part while this one's end is worked on.
 // Which tokens a lane has does not depend on where the row starts, so that
 // equal rows give equal sums and their ties go to the lower beam; a row off a
 // 16-byte boundary is read in aligned groups, two of which make one (ALIGNED:
@@ -499,6 +510,7 @@ struct RowStats {
   Two over;                  // log2 of the sum of 2^(l log2 e - base(top))
   float top;
   float score;               // of the beam
+  float end;                 // the end token's logit, or -inf
 };
 
 // The score of a logit in a row as a key (larger scores have larger keys), 0
@@ -523,9 +535,9 @@ __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
 }
 __device__ __forceinline__ float key_score(u64 k) { return from_ordered((uint32_t)(k >> 32)); }
 
-// A warp per beam, LISTS lists a lane.  What it does takes a few microseconds,
-// most of them for fetching its instructions: so it goes through them once
-// before the parts are there, over made-up lists.
+// A warp per beam, LISTS lists a lane.  Latency alone, and fetching its own
+// instructions is a part of it: so it goes through them once before the parts are
+// there, over made-up lists (half a microsecond less).
 template <typename T, int LISTS>
 __global__ void __launch_bounds__(32 * WQL_MAX_BEAMS) beam_join_kernel(const BeamSelectArgs a) {
   __shared__ RowStats stats[WQL_MAX_BEAMS];
@@ -538,116 +550,120 @@ __global__ void __launch_bounds__(32 * WQL_MAX_BEAMS) beam_join_kernel(const Bea
   griddep_launch_dependents();
   const int beams = a.beams, row0 = blockIdx.x * beams;
   for (int pass = 0; pass < 2; ++pass) {
-  if (pass != 0) griddep_wait();
-  const int parts = pass != 0 ? a.parts : 0;
-  {
-    const int w = warp;
-    const float2* st = a.stats + (size_t)(row0 + w) * parts;
-    const u64* keys = reinterpret_cast<const u64*>(a.keys) + (size_t)(row0 + w) * parts * beams;
-    float2 mine[LISTS];
-    u64 head[LISTS];
-    int at[LISTS];
-    float top = kMinusInf;
-    if (staged) {
-      // the row's lists in shared memory: a list's next key is a step of every
-      // round below
-      u64* own = staged_keys + w * a.parts * beams;
-      for (int i = lane; i < parts * beams; i += 32) own[i] = keys[i];
-      keys = own;
-      __syncwarp();
-    }
+    if (pass != 0) griddep_wait();
+    const int parts = pass != 0 ? a.parts : 0;
+    {
+      const int w = warp;
+      const float2* st = a.stats + (size_t)(row0 + w) * parts;
+      const u64* keys = reinterpret_cast<const u64*>(a.keys) + (size_t)(row0 + w) * parts * beams;
+      // all loads that wait for nothing but the parts
+      float2 mine[LISTS];
 #pragma unroll
-    for (int q = 0; q < LISTS; ++q) {
-      const int p = lane + 32 * q;
-      mine[q] = make_float2(0.f, 1.f);
-      head[q] = make_key((float)lane, 1u);
-      if (pass != 0) {
-        mine[q] = p < parts ? st[p] : make_float2(kMinusInf, 0.f);
-        head[q] = p < parts ? keys[p * beams] : 0ull;
+      for (int q = 0; q < LISTS; ++q) {
+        const int p = lane + 32 * q;
+        mine[q] = make_float2(0.f, 1.f);
+        if (pass != 0) mine[q] = p < parts ? st[p] : make_float2(kMinusInf, 0.f);
       }
-      at[q] = 0;
-    }
-    RowStats r;
-    r.score = pass != 0 ? a.scores[row0 + w] : 0.f;
+      RowStats r;
+      r.score = pass != 0 ? a.scores[row0 + w] : 0.f;
+      r.end = kMinusInf;
+      if (a.ended && a.eos >= 0 && pass != 0)
+        r.end = fmaxf(to_f32(static_cast<const T*>(a.logits)[(size_t)(row0 + w) * a.n + a.eos]), kMinusInf);
+      if (staged) {
+        // the row's lists in shared memory: a list's next key is a step of every
+        // round below
+        u64* own = staged_keys + w * a.parts * beams;
+        for (int i = lane; i < parts * beams; i += 32) own[i] = keys[i];
+        keys = own;
+        __syncwarp();
+      }
+      u64 head[LISTS];
+      int at[LISTS];
+      float top = kMinusInf;
 #pragma unroll
-    for (int q = 0; q < LISTS; ++q) top = fmaxf(top, mine[q].x);
-    top = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(top)));
-    Two sum{0.f, 0.f};
+      for (int q = 0; q < LISTS; ++q) {
+        const int p = lane + 32 * q;
+        head[q] = make_key((float)lane, 1u);
+        if (pass != 0) head[q] = p < parts ? keys[p * beams] : 0ull;
+        at[q] = 0;
+      }
 #pragma unroll
-    for (int q = 0; q < LISTS; ++q)
-      if (mine[q].x > kMinusInf && top < -kMinusInf)
-        sum = add(sum, {mine[q].y * rescale(mine[q].x, top), 0.f});
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-      sum = add(sum, {__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
-    r.top = top;
-    r.over = sum.hi > 0.f ? log2_of(sum) : Two{0.f, 0.f};
-    if (lane == 0) stats[w] = r;
-    // the row's best `beams`, one after another: lane i gets the i-th
-    u64 key = 0ull;
-    for (int i = 0; i < beams; ++i) {
-      u64 k = head[0];
-#pragma unroll
-      for (int q = 1; q < LISTS; ++q) k = head[q] > k ? head[q] : k;
-      const u64 b = warp_max(k);
-      if (b == 0ull) break;
-      if (lane == i) key = b;
+      for (int q = 0; q < LISTS; ++q) top = fmaxf(top, mine[q].x);
+      top = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(top)));
+      Two sum{0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < LISTS; ++q)
-        if (head[q] == b)
-          head[q] = ++at[q] < beams && pass != 0 ? keys[(lane + 32 * q) * beams + at[q]] : 0ull;
+        if (mine[q].x > kMinusInf && top < -kMinusInf)
+          sum = add(sum, {mine[q].y * rescale(mine[q].x, top), 0.f});
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+        sum = add(sum, {__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
+      r.top = top;
+      r.over = sum.hi > 0.f ? log2_of(sum) : Two{0.f, 0.f};
+      if (lane == 0) stats[w] = r;
+      // the row's best `beams`, one after another: lane i gets the i-th
+      u64 key = 0ull;
+      for (int i = 0; i < beams; ++i) {
+        u64 k = head[0];
+#pragma unroll
+        for (int q = 1; q < LISTS; ++q) k = head[q] > k ? head[q] : k;
+        const u64 b = warp_max(k);
+        if (b == 0ull) break;
+        if (lane == i) key = b;
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q)
+          if (head[q] == b)
+            head[q] = ++at[q] < beams && pass != 0 ? keys[(lane + 32 * q) * beams + at[q]] : 0ull;
+      }
+      score[w][lane] = key ? score_of(r, key_logit(key)) : 0ull;
+      token[w][lane] = key_token(key);
     }
-    score[w][lane] = key ? score_of(r, key_logit(key)) : 0ull;
-    token[w][lane] = key_token(key);
-  }
-  __syncthreads();
-  if (warp == 0) {
-  // lane w: beam w's list, best first
-  const bool in = lane < beams;
-  u64 end = 0ull;
-  if (a.ended && in && a.eos >= 0 && pass != 0)
-    end = score_of(stats[lane], fmaxf(to_f32(static_cast<const T*>(a.logits)[(size_t)(row0 + lane) * a.n + a.eos]), kMinusInf));
-  int at = 0, larger = 0;                                  // larger: continuations that beat this beam's end
-  u64 head = in ? score[lane][0] : 0ull, slot_score = 0ull;
-  int found = 0;
-  for (; found < beams; ++found) {
-    const u64 b = warp_max(head);
-    if (b == 0ull) break;
-    larger += b > end;
-    if (lane == found) slot_score = b;
-    // of equal ones the lowest beam
-    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, head == b)) - 1) {
-      place[found] = lane * 32 + at;
-      head = ++at < beams ? score[lane][at] : 0ull;
+    __syncthreads();
+    if (warp == 0) {
+      // lane w: beam w's list, best first
+      const bool in = lane < beams;
+      const u64 end = in ? score_of(stats[lane], stats[lane].end) : 0ull;
+      int at = 0, larger = 0;                                  // larger: continuations that beat this beam's end
+      u64 head = in ? score[lane][0] : 0ull, slot_score = 0ull;
+      int found = 0;
+      for (; found < beams; ++found) {
+        const u64 b = warp_max(head);
+        if (b == 0ull) break;
+        larger += b > end;
+        if (lane == found) slot_score = b;
+        // of equal ones the lowest beam
+        if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, head == b)) - 1) {
+          place[found] = lane * 32 + at;
+          head = ++at < beams ? score[lane][at] : 0ull;
+        }
+      }
+      __syncwarp();
+      const int slot_beam = lane < found ? place[lane] >> 5 : -1;
+      const uint32_t slot_token = lane < found ? token[slot_beam][place[lane] & 31] : 0u;
+      if (a.ended) {
+        for (int i = 0; i < beams; ++i) larger += __shfl_sync(0xFFFFFFFFu, end, i) > end;
+        if (in && pass != 0)
+          a.ended[row0 + lane] = end != 0ull && larger < beams ? key_score(end) : kMinusInf;
+      }
+      int slot = lane;
+      if (a.order == WQL_BEAM_ANCHORED) {
+        // lanes of one beam: the lowest takes its slot, the others the free ones
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, slot_beam);
+        const bool stays = slot_beam >= 0 && __ffs(same) - 1 == lane;
+        const uint32_t taken = __reduce_or_sync(0xFFFFFFFFu, stays ? 1u << slot_beam : 0u);
+        const uint32_t moves = __ballot_sync(0xFFFFFFFFu, !stays);
+        uint32_t open = ~taken;                                // lanes past the beams go past them
+        for (int i = __popc(moves & ((1u << lane) - 1u)); i > 0; --i) open &= open - 1u;
+        slot = stays ? slot_beam : __ffs(open) - 1;
+      }
+      if (in && pass != 0) {
+        const int to = row0 + slot;
+        a.tokens[to] = slot_beam >= 0 ? (int32_t)slot_token : -1;
+        a.parents[to] = slot_beam;
+        a.scores_out[to] = slot_beam >= 0 ? key_score(slot_score) : kMinusInf;
+      }
     }
-  }
-  __syncwarp();
-  const int slot_beam = lane < found ? place[lane] >> 5 : -1;
-  const uint32_t slot_token = lane < found ? token[slot_beam][place[lane] & 31] : 0u;
-  if (a.ended) {
-    for (int i = 0; i < beams; ++i) larger += __shfl_sync(0xFFFFFFFFu, end, i) > end;
-    if (in && pass != 0)
-      a.ended[row0 + lane] = end != 0ull && larger < beams ? key_score(end) : kMinusInf;
-  }
-  int slot = lane;
-  if (a.order == WQL_BEAM_ANCHORED) {
-    // lanes of one beam: the lowest takes its slot, the others the free ones
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, slot_beam);
-    const bool stays = slot_beam >= 0 && __ffs(same) - 1 == lane;
-    const uint32_t taken = __reduce_or_sync(0xFFFFFFFFu, stays ? 1u << slot_beam : 0u);
-    const uint32_t moves = __ballot_sync(0xFFFFFFFFu, !stays);
-    uint32_t open = ~taken;                                // lanes past the beams go past them
-    for (int i = __popc(moves & ((1u << lane) - 1u)); i > 0; --i) open &= open - 1u;
-    slot = stays ? slot_beam : __ffs(open) - 1;
-  }
-  if (in && pass != 0) {
-    const int to = row0 + slot;
-    a.tokens[to] = slot_beam >= 0 ? (int32_t)slot_token : -1;
-    a.parents[to] = slot_beam;
-    a.scores_out[to] = slot_beam >= 0 ? key_score(slot_score) : kMinusInf;
-  }
-  }
-  __syncthreads();
+    __syncthreads();
   }
 }
 

@@ -4,10 +4,18 @@
 //
 // Two launches: lora_down_kernel makes u, lora_up_kernel adds its product.
 // Tokens of one adapter are taken 16 at a time, the rows of one mma.sync
-// m16n8k16; the work is far below what the tensor cores need to be fed from
-// tensor memory for (16 to 64 operations a byte), so both kernels load their
-// fragments from global memory straight into registers: which k a lane's
-// 16 bytes stand for is free, as long as both operands agree.
+// m16n8k16.  The work is far below what the tensor cores need to be fed from
+// tensor memory for (16 to 128 operations a byte; 23 % of the legacy pipe at rank
+// 64): which k a lane's 16 bytes stand for is free, as long as both operands agree,
+// so fragments are 16-byte pieces of rows as they lie.
+//
+// HBM-bound, in the large: b, y and out each move once.  64 rows, each with its
+// own adapter of rank 16, x 248320 x 5120 121 us (67 % of the copy rate); 256 rows, 8
+// adapters of rank 64, x 151936 x 1024 73.5 us (63 %); 4096 rows in 4 runs, rank 32, x
+// 5120 x 5120 41 us (46 %; the two kernels have 16 us each, what the call before wrote
+// is still on its way to memory meanwhile).  One row x 151936 x 1024, rank 16, 5.1 us.
+// What bounds the large ones now is instructions as much as memory: issue 54 %,
+// with 16 warps on an SM.
 #include <type_traits>
 #include <utility>
 
@@ -17,7 +25,7 @@
 namespace wql {
 namespace {
 
-constexpr int kTokens = kLoraSlice;             // a slice of tokens is grouped by adapter at a time
+constexpr int kTokens = kLoraSlice;      // a slice of tokens is grouped by adapter at a time
 constexpr int kDownThreads = 256;
 constexpr int kUpThreads = 256;
 static_assert(kDownThreads == kTokens && kUpThreads == kTokens, "a thread looks at one token of the slice");
@@ -154,11 +162,11 @@ __device__ __forceinline__ void sort_tokens(Sorted& s, const int32_t* ids, int m
 // ---------------------------------------------------------------------------
 // u: a cluster of `splits` blocks per group of tokens, which share the hidden
 // columns; as many clusters as a slice can have groups.  Every block sorts the
-// slice's tokens for itself (a microsecond at most; one list for all would be
-// another launch), the first leaves them for lora_up_kernel.  u is written as
-// the mma fragments that kernel loads: per token, chunk and lane of four, the
-// high parts of four ranks and what they leave of them, and the factor that the
-// products are multiplied with.
+// slice's tokens for itself (0.8 to 2.5 us; one list for all would be another
+// launch).  u is written as the mma fragments that lora_up_kernel loads: per token,
+// chunk and lane of four, the high parts of four ranks and what they leave of them
+// (so that u keeps 16 bits or more), and the factor that the products are
+// multiplied with.
 // ---------------------------------------------------------------------------
 template <typename T, int CHUNKS, int SIZE>
 __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs a, int splits,
@@ -166,10 +174,8 @@ __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs 
   constexpr int kRank = 16 * CHUNKS, kTiles = 2 * CHUNKS, kWarps = kDownThreads / 32;
   constexpr int kBufs = SIZE * kRank > 1024 ? 4 : kWarps;      // 32 KB of sums
   constexpr int kSub = SIZE / 16;        // of the mma's 16 rows
-  constexpr int kLoads = 16;
-  constexpr int kUnits = 2 * kSub + kTiles > kLoads ? 1 : kLoads / (2 * kSub + kTiles);      // of loads at a time
+  constexpr int kUnits = 2 * kSub + kTiles > 16 ? 1 : 16 / (2 * kSub + kTiles);    // 16 loads at a time
   static_assert(SIZE * kRank <= 2048, "sums of four warps");
-  
   __shared__ alignas(16) float part[kBufs][SIZE][kRank];
   __shared__ Sorted sorted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -204,9 +210,8 @@ __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
   // units of 32 columns, 8 a lane, split evenly over the cluster's blocks and
-  // dealt to the warps in turn, so that a block reads a kilobyte of a row at a
-  // time (a range for each warp: pieces of 128 bytes from as many DRAM pages, 25
-  // us instead of 13 for 4096 x 5120)
+  // dealt to the warps in turn; all of a step's loads go out before its products
+  // (left to the compiler, a third of them did: 4096 x 5120 at rank 32 14 us more)
   const int units = (a.k + 31) / 32;
   const int u1 = (int)((long long)units * (split + 1) / splits);
   for (int u = (int)((long long)units * split / splits) + warp * kUnits; u < u1; u += kWarps * kUnits) {
@@ -347,14 +352,6 @@ __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs 
   if (splits > 1) cluster_sync();        // the others have read this block's sums
 }
 
-// ---------------------------------------------------------------------------
-// out = y + factor * u b: a warp has 32 * UNITS columns for a share of a
-// slice's groups, in the order of their adapters, so that it loads b once per
-// adapter.  What a group needs is loaded while the one before it is worked on.
-// The mma's columns are dealt so that a lane ends up with 8 consecutive ones of a
-// token: column j of n-tile i is 8 * (j / 2) + 2 i + j % 2 of the 32.  Rows off
-// a 16-byte boundary (WIDE unset) pass through shared memory, a lane per column.
-// ---------------------------------------------------------------------------
 // The first of a chain: D = A B.
 template <typename T>
 __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -371,6 +368,13 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// ---------------------------------------------------------------------------
+// out = y + factor * u b.  A warp has 32 * UNITS columns and goes through groups in
+// the order of their adapters, so that it reads b once per adapter.  The mma's
+// columns are dealt so that a lane ends up with 8 consecutive ones of a token:
+// column j of n-tile i is 8 * (j / 2) + 2 i + j % 2 of the 32.  Rows off a 16-byte
+// boundary (WIDE unset) pass through shared memory, a lane per column.
+// ---------------------------------------------------------------------------
 // A warp's ring of what groups need, copied ahead: the adapter's b for the
 // warp's columns, where it is another than the group's before, and the rows of y
 // (WIDE).  Both lie so that the eight lanes that are served together find their
