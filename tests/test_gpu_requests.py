@@ -96,14 +96,21 @@ def test_lora_runs_and_leading_shape(dt):
     check_lora(got.view(m, n), y, x, a, b, None, ids, dt)
 
 
-@pytest.mark.parametrize("shift", [1, 4, 7])
-def test_lora_on_any_boundary(shift):
-    y, x, a, b, scale, ids = lora_inputs(21, 72, 64, 16, 2, "bf16", shift)
+@pytest.mark.parametrize("shift,out_shift", [(1, 1), (4, 4), (7, 7), (0, 3), (5, 2), (2, 1)])
+@pytest.mark.parametrize("n", [72, 301, 1, 33, 290])
+def test_lora_on_any_boundary(shift, out_shift, n):
+    """Rows and tensors that start anywhere, y and out apart: what the same
+    columns give in a tensor of whole groups."""
+    wide = (n + 7) // 8 * 8
+    y, x, a, b, scale, ids = lora_inputs(21, wide, 64, 16, 2, "bf16", shift)
     ad = wql.LoraAdapters(a.to(DEV), b.to(DEV), scale.to(DEV))
-    want = wql.wql_lora_add(y.to(DEV), x.to(DEV), ad, ids.to(DEV))
-    out = placed(torch.zeros_like(y), shift)
-    wql.wql_lora_add(placed(y, shift), x.to(DEV), ad, ids.to(DEV), out=out)
+    want = wql.wql_lora_add(y.to(DEV), x.to(DEV), ad, ids.to(DEV))[:, :n]
+    ad = wql.LoraAdapters(a.to(DEV), b[:, :n].contiguous().to(DEV), scale.to(DEV))
+    store = torch.full((21 * n + out_shift + 9,), 7.0, dtype=y.dtype, device=DEV)
+    out = store[out_shift:out_shift + 21 * n].view(21, n)
+    wql.wql_lora_add(placed(y[:, :n].contiguous(), shift), x.to(DEV), ad, ids.to(DEV), out=out)
     assert torch.equal(out, want)
+    assert (store[:out_shift] == 7).all() and (store[out_shift + 21 * n:] == 7).all()
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])

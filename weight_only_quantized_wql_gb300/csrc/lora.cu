@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs 
       for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
   // units of 32 columns, 8 a lane, split evenly over the cluster's blocks and
   // dealt to the warps in turn; all of a step's loads go out before its products
-  // (left to the compiler, a third of them did: 4096 x 5120 at rank 32 14 us more)
+  // (left to the compiler, a third of them did: 4096 x 5120 at rank 32 8 us more)
   const int units = (a.k + 31) / 32;
   const int u1 = (int)((long long)units * (split + 1) / splits);
   for (int u = (int)((long long)units * split / splits) + warp * kUnits; u < u1; u += kWarps * kUnits) {
@@ -418,7 +418,9 @@ template <int N, typename F> __device__ __forceinline__ void for_each(F f) {
 
 
 // A lane's column of a group's rows, four rows at a time; no branch waits for
-// what the ones before it load.
+// what the ones before it load.  (Pairs of columns on 4-byte addresses halve the
+// accesses and cost more in finding them: 200 rows x 151935, rank 32, 90 us for
+// the call, this 75.)
 __device__ __forceinline__ void load_column(const LoraArgs& a, const Sorted& sorted, int base, int p,
                                             int count, int64_t column, uint32_t (&v)[16]) {
   const unsigned short* y = static_cast<const unsigned short*>(a.y) + min(column, (int64_t)a.n - 1);
@@ -632,15 +634,17 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            turn[warp][g][8 * t + 2 * j + e] = f0 * acc[j][e];
-            turn[warp][g + 8][8 * t + 2 * j + e] = f1 * acc[j][2 + e];
+            turn[warp][g][8 * t + 2 * j + e] = acc[j][e];
+            turn[warp][g + 8][8 * t + 2 * j + e] = acc[j][2 + e];
           }
         __syncwarp();
         T* to = static_cast<T*>(a.out) + col0 + lane;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (j >= count) break;
-          if (lane < columns) to[(int64_t)token(p + j) * a.n] = from_f32<T>(low<T>(y[0][j]) + turn[warp][j][lane]);
+          const float f = __shfl_sync(0xFFFFFFFFu, j < 8 ? f0 : f1, 4 * (j & 7));
+          if (lane < columns)
+            to[(int64_t)token(p + j) * a.n] = from_f32<T>(fmaf(f, turn[warp][j][lane], low<T>(y[0][j])));
         }
       }
     }
