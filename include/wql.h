@@ -456,9 +456,10 @@ size_t wql_lora_workspace_size(int64_t m, int32_t rank);
  *   ids  device int32 [m], in any order
  *   y    device [m, n], aligned to its elements (16 bytes and n % 8 == 0 run
  *        faster)
- *   out  device [m, n]; y itself, or apart from it
+ *   out  device [m, n]; y itself, or apart from it (WQL_EINVAL where it shares
+ *        memory with anything else)
  *   workspace  device, 256-byte aligned, ws_bytes >= wql_lora_workspace_size(m,
- *        rank); out must not overlap x, ids, the adapters or the workspace
+ *        rank), apart from all else
  * m <= 2^23. */
 wql_status wql_lora_add(const wql_lora* adapters, const void* x, int64_t m, const int32_t* ids,
                         const void* y, void* out, void* workspace, size_t ws_bytes,
@@ -538,11 +539,11 @@ typedef struct wql_state {
  * read for it nor written.
  *   states   host array of `count` states; different positions and states must
  *            not overlap (checked where states share a span of memory: WQL_EINVAL)
- *   parents  device int32 [batch, beams]
+ *   parents  device int32 [batch, beams]; parents and lengths apart from the states
  *   lengths  device int32 [batch], or NULL
  * beams <= WQL_MAX_BEAMS, batch <= 65535, count <= WQL_MAX_STATES, less than 2^32
- * bytes in a row of a state, strides below 2^40.  16-byte aligned data and
- * strides run faster. */
+ * bytes in a row of a state, strides below 2^40, 2^50 bytes from first to last of
+ * rows, blocks and positions.  16-byte aligned data and strides run faster. */
 wql_status wql_beam_reorder(const wql_state* states, int64_t count, const int32_t* parents,
                             int64_t batch, int64_t beams, const int32_t* lengths,
                             cudaStream_t stream);

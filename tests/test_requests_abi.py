@@ -66,6 +66,27 @@ def test_lora_refusals(lib):
     assert call(n=0, b=None, y=None, out=None, ws=None) == OK
 
 
+def test_lora_out_shares_nothing(lib):
+    """out is y, or apart from everything that the call reads."""
+    at = {"x": 0x100000, "ids": 0x200000, "y": 0x300000, "out": 0x400000, "a": 0x500000,
+          "b": 0x600000, "scale": 0x700000, "ws": 0x800000}
+    m, n, k, count, rank = 3, 100, 64, 4, 16
+    need = wql.wql_lora_workspace_size(m, rank)
+    size = {"x": m * k * 2, "ids": m * 4, "y": m * n * 2, "a": count * rank * k * 2,
+            "b": count * rank * n * 2, "scale": count * 4, "ws": need}
+
+    def call(out):
+        w = wql._WqlLora(F16, rank, count, n, k, at["a"], at["b"], at["scale"])
+        return lib.wql_lora_add(ctypes.byref(w), at["x"], m, at["ids"], at["y"], out, at["ws"],
+                                need, None)
+
+    for name, bytes_ in size.items():
+        assert call(at[name] + bytes_ - 2) == EINVAL, name
+        assert call(at[name] - m * n * 2 + 2) == EINVAL, name
+        if name != "y":
+            assert call(at[name]) == EINVAL, name
+
+
 def test_beam_workspace():
     # 8 bytes and a list of keys for every part of a row
     for b, w, n in ((1, 1, 1), (1, 4, 151936), (64, 4, 151936), (3, 32, 1 << 20)):
@@ -135,6 +156,10 @@ def test_beam_reorder_refusals(lib):
     assert call(one, lengths=A + 2) == EUNSUPPORTED
     assert call(states((A, 1 << 40, 1, 0, 1, 16, 16))) == EUNSUPPORTED
     assert call(states((A, 1 << 33, 1 << 16, 1 << 16, 1 << 16, 1, 1))) == EUNSUPPORTED
+    # spans that no memory has, and whose arithmetic would not fit
+    assert call(states((A, 1 << 39, 1 << 30, 1 << 39, 1, 1, 1))) == EUNSUPPORTED
+    assert call(states((A, 1 << 39, 1, 0, 1 << 30, 1 << 39, 1))) == EUNSUPPORTED
+    assert call(states((A, 1 << 39, 1, 0, 1, 16, 16)), batch=65535) == EUNSUPPORTED
     assert call(one, count=0) == OK
     assert call(one, batch=0) == OK
     assert call(one, beams=1) == OK                       # nothing can move
@@ -207,6 +232,27 @@ def test_overlap_is_brute_force(lib):
         wrong += said and not clash
         sound += not clash
     assert wrong < 0.7 * sound, (wrong, sound)
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 3, 1), (1, 0, 2, 3), (3, 0, 1, 2)])
+def test_layers_of_one_allocation(lib, order):
+    """Rows, heads, positions and layers of one tensor in any order: its layers lie apart,
+    and two that share a byte are found among many."""
+    sizes = (8, 3, 10, 150)
+    stride, size = [0] * 4, 16
+    for d in reversed(order):
+        stride[d] = size
+        size *= sizes[d]
+    layers = [(A + l * stride[3], stride[0], 3, stride[1], 10, stride[2], 16) for l in range(150)]
+    assert not overlapping(lib, *layers)
+    assert not overlapping(lib, *layers[::-1])
+    for l, by in ((0, 8), (70, -8), (149, 8)):
+        moved = list(layers)
+        moved[l] = (layers[l][0] + by, *layers[l][1:])
+        # (the last layer's last byte has nothing behind it, where layers are outermost)
+        if not (l == 149 and by > 0 and order[0] == 3):
+            assert overlapping(lib, *moved), (l, by)
+    assert overlapping(lib, *layers, layers[33])
 
 
 def test_binding_refuses_host_tensors():

@@ -78,6 +78,11 @@ constexpr int64_t kLoraMaxTokens = int64_t(1) << 23;   // 2^15 slices of 256
 constexpr int64_t kBeamMaxRows = int64_t(1) << 20;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether two pieces of memory share a byte (0 bytes: none).
+bool share(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p_bytes > 0 && q_bytes > 0 && a < b + (uintptr_t)q_bytes && b < a + (uintptr_t)p_bytes;
+}
 bool half_dtype(int d) { return d == WQL_F16 || d == WQL_BF16; }
 
 wql_status cuda_fail(cudaError_t e) {
@@ -598,6 +603,13 @@ wql_status wql_lora_add(const wql_lora* w, const void* x, int64_t m, const int32
   const size_t u_bytes = round_up((size_t)m * lora_chunks(w->rank) * 64, 256);
   if (!workspace || ws_bytes < wql_lora_workspace_size(m, w->rank) || !aligned(workspace, 256))
     return WQL_EWORKSPACE;
+  const int64_t out_bytes = m * w->n * 2;              // below 2^55
+  if ((out != y && share(out, out_bytes, y, out_bytes)) || share(out, out_bytes, x, m * w->k * 2) ||
+      share(out, out_bytes, ids, m * 4) || share(out, out_bytes, w->a, w->count * w->rank * w->k * 2) ||
+      share(out, out_bytes, w->b, w->count * w->rank * w->n * 2) ||
+      (w->scale && share(out, out_bytes, w->scale, w->count * 4)) ||
+      share(out, out_bytes, workspace, (int64_t)wql_lora_workspace_size(m, w->rank)))
+    return WQL_EINVAL;
   LoraArgs a{};
   a.a = w->a;
   a.b = w->b;
@@ -678,7 +690,8 @@ wql_status wql_beam_reorder(const wql_state* states, int64_t count, const int32_
   if ((count > 0 && !states) || (count > 0 && batch > 0 && !parents)) return WQL_EINVAL;
   if (beams > WQL_MAX_BEAMS || batch > 65535 || count > WQL_MAX_STATES) return WQL_EUNSUPPORTED;
   if (!aligned(parents, 4) || !aligned(lengths, 4)) return WQL_EUNSUPPORTED;
-  constexpr int64_t kMaxStride = int64_t(1) << 40, kMaxBytes = (int64_t(1) << 32) - 1;
+  constexpr int64_t kMaxStride = int64_t(1) << 40, kMaxSpan = int64_t(1) << 50,
+                    kMaxBytes = (int64_t(1) << 32) - 1;
   for (int64_t i = 0; i < count; ++i) {
     const wql_state& s = states[i];
     if (s.outer < 0 || s.positions < 0 || s.position_bytes < 0 || s.row_stride < 0 ||
@@ -686,6 +699,9 @@ wql_status wql_beam_reorder(const wql_state* states, int64_t count, const int32_
       return WQL_EINVAL;
     const bool empty = s.outer == 0 || s.positions == 0 || s.position_bytes == 0 || batch == 0;
     if (!empty && !s.data) return WQL_EINVAL;
+    if (!empty && (s.outer_stride > kMaxSpan / s.outer || s.position_stride > kMaxSpan / s.positions ||
+                   s.row_stride > kMaxSpan / (batch * beams)))
+      return WQL_EUNSUPPORTED;
     if (s.row_stride >= kMaxStride || s.outer_stride >= kMaxStride || s.position_stride >= kMaxStride)
       return WQL_EUNSUPPORTED;
     if (!empty && (s.outer > kMaxBytes / s.positions ||
