@@ -373,7 +373,7 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
 // the order of their adapters, so that it reads b once per adapter.  The mma's
 // columns are dealt so that a lane ends up with 8 consecutive ones of a token:
 // column j of n-tile i is 8 * (j / 2) + 2 i + j % 2 of the 32.  Rows off a 16-byte
-// boundary (WIDE unset) pass through shared memory, a lane per column.
+// boundary (WIDE unset) pass through shared memory, a lane per column of a unit.
 // ---------------------------------------------------------------------------
 // A warp's ring of what groups need, copied ahead: the adapter's b for the
 // warp's columns, where it is another than the group's before, and the rows of y
@@ -554,10 +554,11 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
       ua[c] = u0[4 * c];
       ub[c] = u1[4 * c];
     }
-    // y: WIDE, rows g and g + 8, 8 columns a unit; else a column a lane
+    // y: WIDE, rows g and g + 8, 8 columns a unit; else a column a lane and unit
     uint32_t y[UNITS][WIDE ? 8 : 16];
-    static_assert(WIDE || UNITS == 1, "a column a lane");
-    if constexpr (!WIDE) load_column(a, sorted, base, p, count, col0 + lane, y[0]);
+    if constexpr (!WIDE)
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) load_column(a, sorted, base, p, count, col0 + 32 * u + lane, y[u]);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const char* slot = mine + offset;
@@ -638,13 +639,13 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
             turn[warp][g + 8][8 * t + 2 * j + e] = acc[j][2 + e];
           }
         __syncwarp();
-        T* to = static_cast<T*>(a.out) + col0 + lane;
+        T* to = static_cast<T*>(a.out) + col0 + 32 * u + lane;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (j >= count) break;
           const float f = __shfl_sync(0xFFFFFFFFu, j < 8 ? f0 : f1, 4 * (j & 7));
-          if (lane < columns)
-            to[(int64_t)token(p + j) * a.n] = from_f32<T>(fmaf(f, turn[warp][j][lane], low<T>(y[0][j])));
+          if (32 * u + lane < columns)
+            to[(int64_t)token(p + j) * a.n] = from_f32<T>(fmaf(f, turn[warp][j][lane], low<T>(y[u][j])));
         }
       }
     }
@@ -678,7 +679,9 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
 
 template <typename T, int CHUNKS, bool WIDE>
 cudaError_t launch_up(const LoraArgs& a, int groups, int slices, cudaStream_t s) {
-  constexpr int kUnits = CHUNKS == 1 && WIDE ? 2 : 1;
+  // (ranks to 16 have registers for two; off the boundary, 64 rows x 50303 with an
+  // adapter each: 40.5 us for the call, 43.5 with one)
+  constexpr int kUnits = CHUNKS == 1 ? 2 : 1;
   using S = Stage<CHUNKS, kUnits, WIDE>;
   constexpr size_t kRing = (size_t)kUpThreads / 32 * S::kStages * S::kBytes;
   auto kern = lora_up_kernel<T, CHUNKS, kUnits, WIDE>;
