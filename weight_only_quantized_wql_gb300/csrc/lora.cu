@@ -418,9 +418,9 @@ template <int N, typename F> __device__ __forceinline__ void for_each(F f) {
 
 
 // A lane's column of a group's rows, four rows at a time; no branch waits for
-// what the ones before it load.  (Pairs of columns on 4-byte addresses halve the
-// accesses and cost more in finding them: 200 rows x 151935, rank 32, 90 us for
-// the call, this 75.)
+// what the ones before it load.  (Pairs of columns on 4-byte addresses, or 16-byte
+// pieces put together in shared memory, save accesses and cost more in finding
+// them: 200 rows x 151935, rank 32, 90 and 79 us for the call, this 77.)
 __device__ __forceinline__ void load_column(const LoraArgs& a, const Sorted& sorted, int base, int p,
                                             int count, int64_t column, uint32_t (&v)[16]) {
   const unsigned short* y = static_cast<const unsigned short*>(a.y) + min(column, (int64_t)a.n - 1);
