@@ -492,6 +492,27 @@ def test_reorder_many_states_of_every_kind():
     check_reorder([(t, t) for t in st], parents, None, None)
 
 
+@pytest.mark.parametrize("beams", [2, 4, 7, 16])
+@pytest.mark.parametrize("some", [False, True])
+def test_reorder_many_columns(beams, some):
+    """Enough to move for a thread to take many pieces of a row: whole ones, ends of
+    rows and of positions, lengths."""
+    batch, l = 64, 40
+    rows = batch * beams
+    g = gen(beams)
+    parents = torch.randint(-1, beams + 1, (batch, beams), generator=g, dtype=torch.int32)
+    parents[0] = torch.arange(beams)
+    lengths = torch.randint(-1, l + 2, (batch,), generator=g, dtype=torch.int32) if some else None
+    big = numbers((rows, 2, l, 264), torch.bfloat16, 1).to(DEV)
+    st = [(big, big)]
+    for i in range(13):
+        gaps = numbers((rows, 3, l, 24), torch.bfloat16, i).to(DEV)
+        thin = numbers((rows, 1, l, 6), torch.uint8, i).to(DEV)
+        ends = numbers((rows, 2, l + 8, 5), torch.float16, i).to(DEV)
+        st += [(gaps, gaps[..., :12]), (thin, thin), (ends, ends[:, :, :l])]
+    check_reorder(st, parents, lengths, 2)
+
+
 def test_reorder_offsets_past_32_bits():
     rows, row = 4, (1 << 31) + 64                         # 8.6 GB
     s = torch.zeros(rows, row, dtype=torch.uint8, device=DEV)
@@ -625,6 +646,60 @@ def test_streams_do_not_disturb_one_another():
     for i in (0, 1):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_graphs_follow_their_inputs():
+    """Two captured graphs, replayed on two streams at once, with other ids, logits and
+    parents than those of the capture."""
+    def inputs(seed):
+        y, x, a, b, scale, ids = lora_inputs(70, 1003, 256, 24, 5, "f16", seed)
+        logits, scores = select_inputs(5, 4, 30001, "f16", seed)
+        cache = numbers((20, 3, 50, 16), torch.float16, seed)
+        return [t.to(DEV) for t in (y, x, ids, logits, scores, cache)], [t.to(DEV) for t in (a, b, scale)]
+
+    def call(ad, y, x, ids, logits, scores, cache):
+        lo = wql.wql_lora_add(y, x, ad, ids)
+        t, parents, s, ended = wql.wql_beam_select(logits, scores, 7, wql.BEAM_ANCHORED)
+        wql.wql_beam_reorder([cache], parents)
+        return lo, t, parents, s, ended, cache
+
+    made = []
+    for i in (0, 1):
+        now, ad = inputs(i)
+        made.append([now, wql.LoraAdapters(*ad)])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call(made[i][1], *now)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call(made[i][1], *now)
+        made[i] += [graph, out, side]
+    for seed in (2, 4, 6):
+        want, new = [], []
+        for i, (now, ad, graph, out, side) in enumerate(made):
+            new.append(inputs(seed + i)[0])
+            want.append([t.clone() for t in call(ad, *[t.clone() for t in new[i]])])
+        torch.cuda.synchronize()
+        for i, (now, ad, graph, out, side) in enumerate(made):
+            with torch.cuda.stream(side):
+                for a, b in zip(now, new[i]):
+                    a.copy_(b)
+                graph.replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(made[i][3], want[i])), (seed, i)
+
+
+def test_lora_out_apart():
+    """An output that overlaps y without being y is refused."""
+    y, x, a, b, scale, ids = (t.to(DEV) for t in lora_inputs(6, 40, 64, 8, 2, "bf16", 8))
+    ad = wql.LoraAdapters(a, b, scale)
+    store = torch.zeros(7, 40, dtype=y.dtype, device=DEV)
+    with pytest.raises(wql.WQLError, match="EINVAL"):
+        wql.wql_lora_add(store[:6], x, ad, ids, out=store[1:])
+    assert not store.any()
 
 
 def test_example_runs():
