@@ -373,7 +373,10 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
 // the order of their adapters, so that it reads b once per adapter.  The mma's
 // columns are dealt so that a lane ends up with 8 consecutive ones of a token:
 // column j of n-tile i is 8 * (j / 2) + 2 i + j % 2 of the 32.  Rows off a 16-byte
-// boundary (WIDE unset) pass through shared memory, a lane per column of a unit.
+// boundary (WIDE unset) pass through shared memory, a lane per column of a unit; what
+// they cost is instructions, so their places are worked out once for a group (4001
+// rows x 24697, rank 8, 175 us for the call, 224 with an address for every access;
+// x 24696 108).
 // ---------------------------------------------------------------------------
 // A warp's ring of what groups need, copied ahead: the adapter's b for the
 // warp's columns, where it is another than the group's before, and the rows of y
@@ -417,19 +420,23 @@ template <int N, typename F> __device__ __forceinline__ void for_each(F f) {
 }
 
 
-// A lane's column of a group's rows, four rows at a time; no branch waits for
-// what the ones before it load.  (Pairs of columns on 4-byte addresses, or 16-byte
-// pieces put together in shared memory, save accesses and cost more in finding
-// them: 200 rows x 151935, rank 32, 90 and 79 us for the call, this 77.)
-__device__ __forceinline__ void load_column(const LoraArgs& a, const Sorted& sorted, int base, int p,
-                                            int count, int64_t column, uint32_t (&v)[16]) {
-  const unsigned short* y = static_cast<const unsigned short*>(a.y) + min(column, (int64_t)a.n - 1);
+// A lane's columns of a group's rows, four rows at a time; no branch waits for
+// what the ones before it load.  `rows`: where the rows lie, in bytes.  (Pairs of
+// columns on 4-byte addresses, or 16-byte pieces put together in shared memory,
+// save accesses and cost more in finding them: 200 rows x 151935, rank 32, 90 and
+// 79 us for the call when this took 77.)
+template <int UNITS>
+__device__ __forceinline__ void load_columns(const char* const (&y)[UNITS], const int64_t* rows, int count,
+                                             uint32_t (&v)[UNITS][16]) {
 #pragma unroll
   for (int j = 0; j < 16; j += 4)
     if (j < count) {
 #pragma unroll
-      for (int i = j; i < j + 4; ++i)          // (past the last row: the last one again)
-        v[i] = __ldcg(y + (int64_t)(base + (int)(sorted.key[p + min(i, count - 1)] & 255u)) * a.n);
+      for (int i = j; i < j + 4; ++i) {
+        const int64_t row = rows[i];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) v[u][i] = __ldcg(reinterpret_cast<const unsigned short*>(y[u] + row));
+      }
     }
 }
 
@@ -440,7 +447,8 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
   constexpr int kFrags = 4 * CHUNKS, kWarps = kUpThreads / 32, kStages = S::kStages;
   extern __shared__ uint4 ring[];              // [warp][stage][S::kBytes]
   __shared__ Sorted sorted;
-  __shared__ float turn[WIDE ? 1 : kWarps][WIDE ? 1 : 16][WIDE ? 1 : 33];
+  __shared__ float turn[WIDE ? 1 : kWarps][WIDE ? 1 : 16][WIDE ? 1 : 32 * UNITS + 1];
+  __shared__ int64_t rows[2][WIDE ? 1 : kWarps][WIDE ? 1 : 16];   // of a group and the next, in bytes
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int base = blockIdx.y * kTokens, m = min(kTokens, a.m - base);
@@ -539,6 +547,9 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
   // where this lane reads: the first piece of a pair that changes places, the other
   const uint32_t b_even = S::b_at(g, 0) + (CHUNKS == 1 ? 8 : 16) * t, b_odd = b_even ^ 64u;
   const uint32_t y_even = S::y_at(g, t), y_odd = S::kSwapY ? y_even ^ 64u : 0u;
+  if (!WIDE && hi > lo && lane < 16)
+    rows[(hi - lo) & 1][warp][lane] = 2 * ((int64_t)token(min(sorted.start[i] + lane, sorted.start[i + 1] - 1)) * a.n);
+  __syncwarp();
   for (int todo = (int)(hi - lo); todo > 0; --todo) {
     const int p = sorted.start[i], count = sorted.start[i + 1] - p;
     const uint32_t id = key_id(sorted.key[p]);
@@ -556,9 +567,18 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
     }
     // y: WIDE, rows g and g + 8, 8 columns a unit; else a column a lane and unit
     uint32_t y[UNITS][WIDE ? 8 : 16];
-    if constexpr (!WIDE)
+    if constexpr (!WIDE) {
+      const char* columns_of[UNITS];           // (past the last column: the last one again)
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) load_column(a, sorted, base, p, count, col0 + 32 * u + lane, y[u]);
+      for (int u = 0; u < UNITS; ++u)
+        columns_of[u] = static_cast<const char*>(a.y) + 2 * min(col0 + 32 * u + lane, (int64_t)a.n - 1);
+      __syncwarp();                            // the group before is stored
+      if (lane < 16 && todo > 1) {
+        const int k = i + 1 == last ? 0 : i + 1, q = sorted.start[k];
+        rows[(todo & 1) ^ 1][warp][lane] = 2 * ((int64_t)token(min(q + lane, sorted.start[k + 1] - 1)) * a.n);
+      }
+      load_columns<UNITS>(columns_of, rows[todo & 1][warp], count, y);
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const char* slot = mine + offset;
@@ -630,22 +650,29 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
             *reinterpret_cast<uint4*>(to + (int64_t)(h ? r1 : r0) * a.n) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       } else {
-        __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            turn[warp][g][8 * t + 2 * j + e] = acc[j][e];
-            turn[warp][g + 8][8 * t + 2 * j + e] = acc[j][2 + e];
+            turn[warp][g][32 * u + 8 * t + 2 * j + e] = acc[j][e];
+            turn[warp][g + 8][32 * u + 8 * t + 2 * j + e] = acc[j][2 + e];
           }
-        __syncwarp();
-        T* to = static_cast<T*>(a.out) + col0 + 32 * u + lane;
+      }
+    }
+    if constexpr (!WIDE) {
+      __syncwarp();
+      char* to = static_cast<char*>(a.out) + 2 * (col0 + lane);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (j >= count) break;
-          const float f = __shfl_sync(0xFFFFFFFFu, j < 8 ? f0 : f1, 4 * (j & 7));
-          if (32 * u + lane < columns)
-            to[(int64_t)token(p + j) * a.n] = from_f32<T>(fmaf(f, turn[warp][j][lane], low<T>(y[u][j])));
+      for (int j = 0; j < 16; j += 4) {
+        if (j >= count) break;
+#pragma unroll
+        for (int r = j; r < j + 4; ++r) {
+          const float f = __shfl_sync(0xFFFFFFFFu, r < 8 ? f0 : f1, 4 * (r & 7));
+          T* at = reinterpret_cast<T*>(to + rows[todo & 1][warp][r]);
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u)
+            if (r < count && 32 * u + lane < columns)
+              at[32 * u] = from_f32<T>(fmaf(f, turn[warp][r][32 * u + lane], low<T>(y[u][r])));
         }
       }
     }
@@ -679,9 +706,10 @@ __global__ void __launch_bounds__(kUpThreads, CHUNKS <= 4 ? 2 : 1)
 
 template <typename T, int CHUNKS, bool WIDE>
 cudaError_t launch_up(const LoraArgs& a, int groups, int slices, cudaStream_t s) {
-  // (ranks to 16 have registers for two; off the boundary, 64 rows x 50303 with an
-  // adapter each: 40.5 us for the call, 43.5 with one)
-  constexpr int kUnits = CHUNKS == 1 ? 2 : 1;
+  // (as ranks leave registers for two.  Off the boundary 64 rows x 50303 with an
+  // adapter each, rank 16: 41 us for the call, 43.5 with one; 1000 rows x 50303, rank
+  // 32: 117, 132 with one.)
+  constexpr int kUnits = CHUNKS == 1 || (CHUNKS == 2 && !WIDE) ? 2 : 1;
   using S = Stage<CHUNKS, kUnits, WIDE>;
   constexpr size_t kRing = (size_t)kUpThreads / 32 * S::kStages * S::kBytes;
   auto kern = lora_up_kernel<T, CHUNKS, kUnits, WIDE>;
