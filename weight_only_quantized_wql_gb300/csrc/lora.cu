@@ -10,7 +10,7 @@
 // so fragments are 16-byte pieces of rows as they lie.
 //
 // HBM-bound, in the large: b, y and out each move once.  64 rows, each with its
-// own adapter of rank 16, x 248320 x 5120 120 us (68 % of the copy rate); 256 rows, 8
+// own adapter of rank 16, x 248320 x 5120 120 us (67 % of the copy rate); 256 rows, 8
 // adapters of rank 64, x 151936 x 1024 73.5 us (63 %); 4096 rows in 4 runs, rank 32, x
 // 5120 x 5120 41 us (46 %; the first kernel, which reads a again for every 16 rows from
 // L2, has half of it).  One row x 151936 x 1024, rank 16, 5.1 us.
