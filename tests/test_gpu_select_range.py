@@ -1,0 +1,83 @@
+"""Beam selection on logits of every finite size, against the 64-bit reference
+(ref_requests.py): masks of large finite values, large maxima, rows masked throughout."""
+import numpy as np
+import pytest
+import torch
+
+import ref_requests as ref
+import weight_only_quantized_wql_gb300 as wql
+from ref64 import f64
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+T = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+ORDERS = [wql.BEAM_RANKED, wql.BEAM_ANCHORED]
+
+# The error of a score before its rounding.  Of the logarithm of the sum: a term is
+# an exponential (2^-22) and passes at most 16 rescalings in its lane and three in the
+# joins (2^-22 each); the arguments' roundings, two of each part of d = top - l and
+# log2 e's own, add up to 2^-23 d + 2^-26 d, d's mean under the softmax being at most
+# log n < 14; at most 65 additions on a term's way, 2^-24 each; the logarithm's
+# mantissa 2^-23.  In rows far from zero the exponents hold a rounding R of the
+# maximum's product besides, 2^-24 R (R <= 10 where logits are less than 14 apart), and
+# products in two parts 2^-24.  In two fp32 parts a score of size s is off by 2^-45 s more.
+SCORE = 20 * 2.0 ** -22 + 14 * (2.0 ** -23 + 2.0 ** -26) + 76 * 2.0 ** -24 + 2.0 ** -23
+PARTS = 2.0 ** -45
+
+
+def compare(logits, scores, eos, order):
+    """A call against the reference; False where the inputs decide something by less
+    than the errors."""
+    tokens, parents, best, ended, gap = ref.beam_select(f64(logits), f64(scores), -1 if eos is None else eos,
+                                                        order == wql.BEAM_ANCHORED)
+    sizes = [np.abs(v[np.isfinite(v)]).max(initial=0.0) for v in (best, ended)]
+    if gap <= 2 * (SCORE + PARTS * max(sizes)):
+        return False
+    t, p, s, e = wql.wql_beam_select(logits.to(DEV), scores.to(DEV), eos, order)
+
+    def near(x, want):
+        x, fine = f64(x), np.isfinite(want)
+        np.testing.assert_array_equal(np.isfinite(x), fine)
+        assert np.all(x[~fine] == -np.inf)
+        err = np.abs(x[fine] - want[fine])
+        tol = SCORE + (PARTS + 2.0 ** -24) * np.abs(want[fine])
+        assert np.all(err <= tol), (err - tol).max()
+
+    near(s, best)
+    if eos is not None:
+        near(e, ended)
+    np.testing.assert_array_equal(t.cpu().numpy(), tokens)
+    np.testing.assert_array_equal(p.cpu().numpy(), parents)
+    return True
+
+
+def first_clear(make, eos, order):
+    for seed in range(20):
+        if compare(*make(seed), eos, order):
+            return
+    raise AssertionError("no clear inputs")
+
+
+def inputs(batch, beams, n, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+    logits = (3 * torch.randn(batch, beams, n, generator=g)).to(T[dt])
+    scores = -torch.rand(batch, beams, generator=g).cumsum(-1) * 2
+    return g, logits, scores
+
+
+# ---------------------------------------------------------------------------
+# Rows far from zero
+# ---------------------------------------------------------------------------
+CENTERS = [("f16", 300.0), ("f16", 1000.0), ("f16", 3e4), ("bf16", 300.0), ("bf16", 1000.0)]
+CENTERS += [("f32", c) for c in (300.0, 1000.0, 3e4, 7e5, 3e6, 3e7)]
+
+
+@pytest.mark.parametrize("dt,center", CENTERS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_differences_of_large_logits(dt, center, sign):
+    """Rows far from zero whose logits differ by ordinary amounts."""
+    def make(seed):
+        _, logits, scores = inputs(80, 4, 20000, dt, seed)
+        return (logits.float() + sign * center).to(T[dt]), scores
+
+    first_clear(make, 19, wql.BEAM_RANKED)

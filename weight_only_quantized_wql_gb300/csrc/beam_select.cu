@@ -72,10 +72,11 @@ __device__ __forceinline__ float ex2(float v) {
 
 // Exponentials are taken as 2^(l * log2 e - base(m)) over a maximum m: one
 // fused multiply-add, whose base is an fp32 number, so that its rounding is
-// none of the sum's.  Where m * log2 e would overflow, the difference to m is
-// taken first.
+// none of the sum's (as long as all take the same one: a product that the compiler
+// fuses into a difference of two bases is not rounded).  Where m * log2 e would
+// overflow, the difference to m is taken first.
 __device__ __forceinline__ bool plain(float m) { return fabsf(m) < 2e38f; }
-__device__ __forceinline__ float base(float m) { return m * kLog2e; }
+__device__ __forceinline__ float base(float m) { return __fmul_rn(m, kLog2e); }
 __device__ __forceinline__ double base64(float m) {
   return plain(m) ? (double)base(m) : (double)m * (double)kLog2e;
 }
