@@ -24,6 +24,8 @@ ORDERS = [wql.BEAM_RANKED, wql.BEAM_ANCHORED]
 SCORE = 20 * 2.0 ** -22 + 14 * (2.0 ** -23 + 2.0 ** -26) + 76 * 2.0 ** -24 + 2.0 ** -23
 PARTS = 2.0 ** -45
 
+LOWEST = {k: torch.finfo(v).min for k, v in T.items()}
+
 
 def compare(logits, scores, eos, order):
     """A call against the reference; False where the inputs decide something by less
@@ -81,3 +83,25 @@ def test_differences_of_large_logits(dt, center, sign):
         return (logits.float() + sign * center).to(T[dt]), scores
 
     first_clear(make, 19, wql.BEAM_RANKED)
+
+
+# ---------------------------------------------------------------------------
+# Rows that are masked throughout
+# ---------------------------------------------------------------------------
+def check_whole_rows(dt, mask, order, n):
+    """Every token of a masked row has the probability 1 / n."""
+    def make(seed):
+        _, logits, scores = inputs(4, 4, n, dt, seed)
+        logits[0, 1] = mask
+        logits[1, :3] = mask
+        logits[2] = mask
+        return logits, scores
+
+    first_clear(make, 3, order)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt", T)
+@pytest.mark.parametrize("n", [5, 20000])
+def test_whole_rows_of_the_lowest_value(dt, order, n):
+    check_whole_rows(dt, LOWEST[dt], order, n)

@@ -529,8 +529,9 @@ __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
     const float q = __fmul_rn(d.hi, kLn2);
     s = add(s, normal(q, fmaf(d.lo, kLn2, fmaf(d.hi, kLn2Rest, fmaf(d.hi, kLn2, -q)))));
   } else {                   // a row of masks
-    const double over = base64(r.top) + ((double)r.over.hi + (double)r.over.lo);
-    s = split((double)r.score + ((double)l * (double)kLog2e - over) * 0.69314718055994530942);
+    // (the maximum first: the logarithm of the sum would be lost beside it)
+    const double d = ((double)l * (double)kLog2e - base64(r.top)) - ((double)r.over.hi + (double)r.over.lo);
+    s = split((double)r.score + d * 0.69314718055994530942);
   }
   return (u64)ordered(s.hi + 0.f) << 32 | ordered(s.lo + 0.f);
 }
