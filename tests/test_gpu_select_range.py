@@ -25,6 +25,9 @@ SCORE = 20 * 2.0 ** -22 + 14 * (2.0 ** -23 + 2.0 ** -26) + 76 * 2.0 ** -24 + 2.0
 PARTS = 2.0 ** -45
 
 LOWEST = {k: torch.finfo(v).min for k, v in T.items()}
+LARGE = [-1e4, -1e9, -1e10, -1e11, -1e12, -1e20, -1e30, -1e38, -2.2e38]
+MASKS = [(dt, m) for dt in ("f32", "bf16") for m in LARGE + [LOWEST[dt] / 2, LOWEST[dt]]]
+MASKS += [("f16", -1e4), ("f16", LOWEST["f16"])]
 
 
 def compare(logits, scores, eos, order):
@@ -105,3 +108,71 @@ def check_whole_rows(dt, mask, order, n):
 @pytest.mark.parametrize("n", [5, 20000])
 def test_whole_rows_of_the_lowest_value(dt, order, n):
     check_whole_rows(dt, LOWEST[dt], order, n)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt,mask", MASKS)
+@pytest.mark.parametrize("n", [5, 20000])
+def test_whole_rows_masked(dt, mask, order, n):
+    check_whole_rows(dt, mask, order, n)
+
+
+# ---------------------------------------------------------------------------
+# Rows that are masked in part, and large maxima
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt,mask", MASKS)
+def test_few_tokens_allowed(dt, mask, order):
+    """Six tokens of 20000 (the first, the last and the end token among them): whole
+    lanes, warps and parts see nothing but the mask."""
+    def make(seed):
+        g, logits, scores = inputs(4, 4, 20000, dt, seed)
+        allowed = torch.zeros(4, 4, 20000, dtype=torch.bool)
+        allowed.scatter_(-1, torch.randint(1, 19999, (4, 4, 3), generator=g), True)
+        allowed[..., [0, 77, -1]] = True
+        return logits.masked_fill(~allowed, mask), scores
+
+    first_clear(make, 77, order)
+
+
+@pytest.mark.parametrize("dt,mask", MASKS)
+def test_lanes_masked_before_and_after(dt, mask):
+    """Rows of several steps, the first, the last or every other stretch of them masked."""
+    def make(seed):
+        _, logits, scores = inputs(80, 4, 20000, dt, seed)
+        logits[0::4, :, :10000] = mask
+        logits[1::4, :, 10000:] = mask
+        for at in range(0, 20000, 1024):
+            logits[2::4, :, at:at + 512] = mask
+        return logits, scores
+
+    first_clear(make, 19, wql.BEAM_RANKED)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [2e6, 1e10, 1e30, 1e38, 2.2e38, 3e38])
+def test_large_maxima(dt, top, order):
+    """Six equal maxima in half of the rows: they share the probability."""
+    def make(seed):
+        g, logits, scores = inputs(3, 4, 20000, dt, seed)
+        logits[:, ::2].scatter_(-1, torch.randint(0, 20000, (3, 2, 6), generator=g), top)
+        logits[2, :, 5000:] = -top
+        return logits, scores
+
+    first_clear(make, None, order)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_maxima_on_both_sides_of_the_border(sign, order):
+    """Lanes' maxima next to 2^31 / log2 e, where the sums change their form; one step
+    of fp32 is 128 there."""
+    def make(seed):
+        g, logits, scores = inputs(3, 4, 20000, "f32", seed)
+        steps = torch.randint(0, 3, (3, 4, 20000), generator=g) - 4
+        steps.scatter_(-1, torch.randint(0, 20000, (3, 4, 6), generator=g), 2)
+        steps[0, 0] = torch.randint(-2, 3, (20000,), generator=g)
+        return (sign * 1488522240.0 + 128 * steps.double()).float(), scores
+
+    first_clear(make, None, order)

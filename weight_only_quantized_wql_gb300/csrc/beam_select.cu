@@ -73,17 +73,25 @@ __device__ __forceinline__ float ex2(float v) {
 // Exponentials are taken as 2^(l * log2 e - base(m)) over a maximum m: one
 // fused multiply-add, whose base is an fp32 number, so that its rounding is
 // none of the sum's (as long as all take the same one: a product that the compiler
-// fuses into a difference of two bases is not rounded).  Where m * log2 e would
-// overflow, the difference to m is taken first.
-__device__ __forceinline__ bool plain(float m) { return fabsf(m) < 2e38f; }
+// fuses into a difference of two bases is not rounded).  At l = m the exponent is that
+// rounding, up to half a unit in base's last place, not 0.  Below 2^31 it is at most 64,
+// so that sums of 2^20 terms stay in fp32's range (and where it is more than 10, logits
+// lie more than 14 apart); from there on, which takes masks of large finite values,
+// exponentials are 2^((l - m) * log2 e).  m alone decides.
+constexpr float kPlain = 2147483648.f;
+__device__ __forceinline__ bool plain_base(float b) { return fabsf(b) < kPlain; }
 __device__ __forceinline__ float base(float m) { return __fmul_rn(m, kLog2e); }
+__device__ __forceinline__ bool plain(float m) { return plain_base(base(m)); }
 __device__ __forceinline__ double base64(float m) {
   return plain(m) ? (double)base(m) : (double)m * (double)kLog2e;
 }
 // What a sum over `from` is multiplied with to be one over `to`, from <= to.
 __device__ __forceinline__ float rescale(float from, float to) {
   if (from == to) return 1.f;
-  return plain(from) && plain(to) ? ex2(base(from) - base(to)) : ex2((from - to) * kLog2e);
+  const float a = base(from), b = base(to);
+  const bool p = plain_base(a), q = plain_base(b);
+  // each less what it is held over
+  return ex2(fmaf((p ? 0.f : from) - (q ? 0.f : to), kLog2e, (p ? a : 0.f) - (q ? b : 0.f)));
 }
 
 // Two floats in one register pair.
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_part_kernel(const Be
       float p0, p1;
       unpair2(add2(part0, part1), p0, p1);
       float more = p0 + p1;
-      if (!(more <= kLargest) && m < -kMinusInf) {         // NaN among them, or m is too large
+      if (!(more <= kLargest && plain_base(over))) {       // NaN among them, or m is far from zero
         more = 0.f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
@@ -498,8 +506,8 @@ __device__ __forceinline__ Two split(double v) {
   return {hi, (float)(v - (double)hi)};
 }
 
-// log2(t) for t in [1, 2^31): the exponent and the logarithm of what is left,
-// which lies in [0, 1].
+// log2(t) for a normal t: the exponent and the logarithm of what is left, which lies
+// in [0, 1].
 __device__ __forceinline__ Two log2_of(Two t) {
   const int e = (int)(__float_as_uint(t.hi) >> 23) - 127;
   const float m = __uint_as_float((__float_as_uint(t.hi) & 0x007FFFFFu) | 0x3F800000u);
@@ -522,13 +530,13 @@ __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
   Two s{r.score, 0.f};
   if (r.top == -kMinusInf) {
     if (l != r.top) return 0ull;
-  } else if (fabsf(l) < 1e38f && fabsf(r.top) < 1e38f) {
+  } else if (fabsf(l) < 1e38f && plain(r.top)) {
     const float p = __fmul_rn(l, kLog2e);
     const Two d = add(add({p, fmaf(l, kLog2e, -p)}, {-base(r.top), 0.f}), {-r.over.hi, -r.over.lo});
     constexpr float kLn2 = 0.693147180559945f, kLn2Rest = (float)(0.69314718055994530942 - (double)kLn2);
     const float q = __fmul_rn(d.hi, kLn2);
     s = add(s, normal(q, fmaf(d.lo, kLn2, fmaf(d.hi, kLn2Rest, fmaf(d.hi, kLn2, -q)))));
-  } else {                   // a row of masks
+  } else {                   // a row of masks, or a masked token of the lowest values
     // (the maximum first: the logarithm of the sum would be lost beside it)
     const double d = ((double)l * (double)kLog2e - base64(r.top)) - ((double)r.over.hi + (double)r.over.lo);
     s = split((double)r.score + d * 0.69314718055994530942);
