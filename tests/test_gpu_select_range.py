@@ -176,3 +176,29 @@ def test_maxima_on_both_sides_of_the_border(sign, order):
         return (sign * 1488522240.0 + 128 * steps.double()).float(), scores
 
     first_clear(make, None, order)
+
+
+# ---------------------------------------------------------------------------
+# Scores far below the best
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("order", ORDERS)
+def test_beams_meet_far_below_the_best(order):
+    """A beam 5000 below another continues before that one's token 5000 below its best,
+    by 3e-5."""
+    logits = torch.full((1, 2, 40), -torch.inf)
+    logits[0, :, 0] = 0.0
+    logits[0, 1, 1] = -5000.0
+    scores = torch.tensor([[-5000.0, -3e-5]])
+    assert compare(logits, scores, None, order)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt,mask", MASKS)
+def test_masked_tokens_are_selected(dt, mask, order):
+    """Fewer allowed tokens than beams, and one beam: masked ones follow, the lowest first."""
+    _, logits, scores = inputs(2, 4, 3000, dt, 0)
+    allowed = torch.zeros(3000, dtype=torch.bool)
+    allowed[[1, 2999]] = True
+    logits.masked_fill_(~allowed, mask)
+    scores[:, 0], scores[:, 1:] = -1.25, -torch.inf
+    assert compare(logits, scores, 2, order)

@@ -522,9 +522,12 @@ struct RowStats {
   float end;                 // the end token's logit, or -inf
 };
 
+// log2 e is fp32's in the sums and here, and scores are divided by the same: of l - top
+// nothing is lost, and the logarithm of the sum is off by 1.3e-8 of the mean of top - l.
+constexpr double kPerLog2 = 1.0 / (double)kLog2e;
+
 // The score of a logit in a row as a key (larger scores have larger keys), 0
-// where it does not continue the beam.  (log2 e is fp32's in the sums and here,
-// so that the difference is one of 1.3e-8 of the logarithm of the probability.)
+// where it does not continue the beam.
 __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
   if (!(fabsf(r.score) <= kLargest) || !(l > kMinusInf)) return 0ull;
   Two s{r.score, 0.f};
@@ -533,13 +536,13 @@ __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
   } else if (fabsf(l) < 1e38f && plain(r.top)) {
     const float p = __fmul_rn(l, kLog2e);
     const Two d = add(add({p, fmaf(l, kLog2e, -p)}, {-base(r.top), 0.f}), {-r.over.hi, -r.over.lo});
-    constexpr float kLn2 = 0.693147180559945f, kLn2Rest = (float)(0.69314718055994530942 - (double)kLn2);
-    const float q = __fmul_rn(d.hi, kLn2);
-    s = add(s, normal(q, fmaf(d.lo, kLn2, fmaf(d.hi, kLn2Rest, fmaf(d.hi, kLn2, -q)))));
+    constexpr float kPer = (float)kPerLog2, kPerRest = (float)(kPerLog2 - (double)kPer);
+    const float q = __fmul_rn(d.hi, kPer);
+    s = add(s, normal(q, fmaf(d.lo, kPer, fmaf(d.hi, kPerRest, fmaf(d.hi, kPer, -q)))));
   } else {                   // a row of masks, or a masked token of the lowest values
     // (the maximum first: the logarithm of the sum would be lost beside it)
     const double d = ((double)l * (double)kLog2e - base64(r.top)) - ((double)r.over.hi + (double)r.over.lo);
-    s = split((double)r.score + d * 0.69314718055994530942);
+    s = split((double)r.score + d * kPerLog2);
   }
   return (u64)ordered(s.hi + 0.f) << 32 | ordered(s.lo + 0.f);
 }
