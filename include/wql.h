@@ -491,9 +491,9 @@ size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n);
  * continuations the best `beams` whose token is not `eos` are selected: score
  * descending, then beam ascending, then, within a beam, logit descending and
  * token ascending.
- *   A logit of -inf, or NaN, gives no continuation.  In a row with logits of +inf
- *   those score scores[w] and no other continues.  A beam whose score is not finite
- *   has no continuations.  Where fewer than `beams` are left, the rest of the slots
+ *   A logit of -inf, or NaN, gives no continuation, nor does one whose s lies below
+ *   fp32's range.  In a row with logits of +inf those score scores[w] and no other
+ *   continues.  A beam whose score is not finite has no continuations.  Where fewer than `beams` are left, the rest of the slots
  *   (the free ones in ascending order) get token -1, parent -1 and score -inf.
  *   logits       device [batch, beams, n] of dtype (F32, F16 or BF16), aligned to
  *                its elements

@@ -202,3 +202,34 @@ def test_masked_tokens_are_selected(dt, mask, order):
     logits.masked_fill_(~allowed, mask)
     scores[:, 0], scores[:, 1:] = -1.25, -torch.inf
     assert compare(logits, scores, 2, order)
+
+
+# ---------------------------------------------------------------------------
+# Scores below fp32's range
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", [-9e37, -1.7e38, -3e38])
+def test_scores_below_the_range(dt, mask, order):
+    """The lowest finite score and masked tokens: their sum rounds to -inf, which is no
+    continuation; nor does a beam end with it."""
+    logits = torch.full((1, 3, 50), mask).to(T[dt])
+    logits[0, :2, 5] = 2.0                      # the end token: all that is left of beam 1
+    logits[0, 0, 7] = 1.0
+    logits[0, 2, 9] = 0.0
+    low = torch.finfo(torch.float32).min
+    t, p, s, e = wql.wql_beam_select(logits.to(DEV), torch.tensor([[0.0, low, low]], device=DEV), 5, order)
+    # beam 0's two, its masked ones with a finite score; beam 2's token 9
+    assert t.tolist() == [[7, 0, 1]] and p.tolist() == [[0, 0, 0]]
+    assert torch.isfinite(s).all()
+    lse = np.log(np.exp(2.0) + np.exp(1.0))
+    assert abs(s[0, 0].item() - (1.0 - lse)) <= 1e-5 and abs(e[0, 0].item() - (2.0 - lse)) <= 1e-5
+    assert torch.all(s[0, 1:] == logits[0, 0, 0].float().item())
+    # beam 1 alone: what it has is its end; beam 2: one token
+    t, p, s, e = wql.wql_beam_select(logits[:, 1:].to(DEV), torch.tensor([[low, low]], device=DEV), 5, order)
+    at = 1 if order == wql.BEAM_ANCHORED else 0
+    want = [[-1, -1]]
+    want[0][at] = 9
+    assert t.tolist() == want and p.tolist() == [[1 if v == 9 else -1 for v in want[0]]]
+    assert s[0, at].item() == low and s[0, 1 - at].item() == -np.inf
+    assert e[0, 0].item() == low and e[0, 1].item() == -np.inf

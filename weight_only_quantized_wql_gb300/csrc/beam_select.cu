@@ -544,6 +544,7 @@ __device__ __forceinline__ u64 score_of(const RowStats& r, float l) {
     const double d = ((double)l * (double)kLog2e - base64(r.top)) - ((double)r.over.hi + (double)r.over.lo);
     s = split((double)r.score + d * kPerLog2);
   }
+  if (!(s.hi >= -kLargest)) return 0ull;                     // below fp32's range, or NaN of its sums
   return (u64)ordered(s.hi + 0.f) << 32 | ordered(s.lo + 0.f);
 }
 __device__ __forceinline__ float key_score(u64 k) { return from_ordered((uint32_t)(k >> 32)); }
