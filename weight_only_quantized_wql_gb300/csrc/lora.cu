@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(kDownThreads) lora_down_kernel(const LoraArgs 
       const int e2 = min(max((int)(top >> 23), 1), 253);      // biased; u = 0: anything
       const float down = __uint_as_float((uint32_t)(254 - e2) << 23);
       factor = scale * __uint_as_float((uint32_t)e2 << 23);
+      // a finite scale stays finite: an infinite one would make sums that are 0 NaN (all
+      // others, multiples of 2^-48, overflow the result with this one too)
+      if (fabsf(scale) <= 3.4028235e38f) factor = fminf(fmaxf(factor, -3.4028235e38f), 3.4028235e38f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] *= down;
     }
