@@ -485,16 +485,20 @@ size_t wql_beam_workspace_size(int64_t batch, int64_t beams, int64_t n);
 /* One step of beam search for `batch` sequences of `beams` beams each.  The
  * continuation of beam w by token v scores
  *   s[w, v] = scores[w] + l[w, v] - log sum_v' exp(l[w, v']),
- * l the logits: exponentials in fp32 and sums of them over parts of a row, the
- * sums over the parts and the scores in two fp32 parts (some 46 bits), rounded to
- * fp32 at the end; scores are compared before that.  Of a sequence's beams * n
- * continuations the best `beams` whose token is not `eos` are selected: score
- * descending, then beam ascending, then, within a beam, logit descending and
- * token ascending.
+ * l the logits, of any finite size: exponentials and their sums over parts of a row
+ * in fp32, joined, with the logits' distances and the scores, in two fp32 parts (some
+ * 46 bits), rounded to fp32 at the end; scores are compared before that.  The logarithm
+ * of a row's sum has fp32's error, below 1.2e-5 (3.5e-7 as measured): inside a
+ * beam the order is the logits' own, scores of different beams that lie nearer to one
+ * another may be ordered either way (those of equal rows and scores are equal).  Of a
+ * sequence's beams * n continuations the best `beams` whose token is not `eos` are
+ * selected: score descending, then beam ascending, then, within a beam, logit
+ * descending and token ascending.
  *   A logit of -inf, or NaN, gives no continuation, nor does one whose s lies below
  *   fp32's range.  In a row with logits of +inf those score scores[w] and no other
- *   continues.  A beam whose score is not finite has no continuations.  Where fewer than `beams` are left, the rest of the slots
- *   (the free ones in ascending order) get token -1, parent -1 and score -inf.
+ *   continues.  A beam whose score is not finite has no continuations.  Where fewer
+ *   than `beams` are left, the rest of the slots (the free ones in ascending order)
+ *   get token -1, parent -1 and score -inf.
  *   logits       device [batch, beams, n] of dtype (F32, F16 or BF16), aligned to
  *                its elements
  *   scores       device float [batch, beams]: log-probabilities of the beams (for

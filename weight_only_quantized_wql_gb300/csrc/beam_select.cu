@@ -12,11 +12,12 @@
 // depend on the order in which lists were filled.
 //
 // HBM-bound, where there are logits enough: 16 sequences x 16 beams x 248320 fp32
-// 53.5 us (70 % of the copy rate), 64 x 4 x 151936 bf16 24.3 us (47 %): its logits
+// 54.7 us (68 % of the copy rate), 64 x 4 x 151936 bf16 24.6 us (47 %): its logits
 // arrive in 11 to 14 us, at the copy rate; 3.5 us follow for the ends of the
-// parts, 1 for the second launch and 3 for the joining.  1 x 4 x 151936 bf16 7.7
+// parts, 1 for the second launch and 3 for the joining.  1 x 4 x 151936 bf16 7.6
 // us, 7 x 5 x 50303 fp16 10.0 us, of which the two launches and their dependent
-// steps are all.
+// steps are all.  All but a thousandth masked by -1e9 or -inf costs nothing more; by a
+// value beyond -1.4e9, whose exponentials take the slower form, 64 x 4 x 151936 38.5.
 #include "requests.cuh"
 #include "sm100.cuh"
 
@@ -484,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, kResident) beam_part_kernel(const Be
 // One sequence.
 // ---------------------------------------------------------------------------
 // Sums and scores are held in two fp32 parts, hi the nearest fp32 number and lo
-// the rest: some 46 bits.  (In binary64 a sequence of 16 beams took 4 us more:
-// the SM does two such operations a cycle.)
+// the rest: some 46 bits, which keep the logits' order and their distances; the parts'
+// sums and the logarithm of the row's are fp32's.  (In binary64 a sequence of 16 beams
+// took 4 us more: the SM does two such operations a cycle.)
 struct Two {
   float hi, lo;
 };

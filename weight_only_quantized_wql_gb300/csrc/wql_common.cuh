@@ -432,8 +432,13 @@ __device__ __forceinline__ unsigned long long pick(const unsigned long long (&v)
 // start while the preceding kernel on the stream finishes; each reads
 // nothing another kernel may write (its inputs, the workspace) and writes
 // nothing before griddep_wait(), which returns once the preceding kernel has
-// completed and its writes are visible (the decode kernel's early weight
-// copies under WQL_WEIGHT_STATIC are the one documented exception).
+// completed and its writes are visible.  Two exceptions: the decode kernel's
+// early weight copies under WQL_WEIGHT_STATIC, and lora_up_kernel, which reads
+// ids, y and b before it.  That is sound only because lora_down_kernel, always
+// the kernel before, calls griddep_launch_dependents() after its own
+// griddep_wait(): when lora_up_kernel begins, all kernels before the two are
+// done and seen (and it reads past the L1).  It reads nothing of
+// lora_down_kernel's, and writes nothing, before its wait.
 // griddep_launch_dependents() lets the following kernel launch early.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void griddep_wait() {
